@@ -90,6 +90,16 @@ _SIGS = {
     "lbq_moe_align": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _vp], _c_int),
     "lbq_moe_lut3_mx_gemm": ([_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _vp, _c_size, _c_int,
                               _vp, _c_int, _vp], _c_int),
+    "lbq_quantize_int8_rows": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp], _c_int),
+    "lbq_quantize_int8_weight": ([_vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
+    "lbq_w8a8_gemm": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _vp], _c_int),
+    "lbq_w8a8_workspace_size": ([_c_int, _c_int, ctypes.POINTER(_c_size)], _c_int),
+    "lbq_w8a8_linear": ([_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp], _c_int),
+    "lbq_moe_w8a8_gemm": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp, _c_int, _vp], _c_int),
+    "lbq_moe_sort": ([_vp, _c_int, _c_int, _vp, _vp, _vp, _vp], _c_int),
+    "lbq_moe_permute": ([_vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp], _c_int),
+    "lbq_moe_combine": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp], _c_int),
+    "lbq_moe_combine_grad": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "lbq_debug_force_splits": ([_c_int], None),
     "lbq_debug_force_skinny": ([_c_int], None),
     "lbq_debug_force_tc": ([_c_int], None),
@@ -324,6 +334,48 @@ def lbq_moe_lut3_mx_gemm(codes, scales, T, top_k, K, N, sorted_ids, expert_ids, 
                          image_stride, num_local_experts, Y, y_dtype, stream):
     _check(_lib.lbq_moe_lut3_mx_gemm(codes, scales, T, top_k, K, N, sorted_ids, expert_ids, total, max_padded, images,
                                      image_stride, num_local_experts, Y, y_dtype, stream))
+
+
+def lbq_quantize_int8_rows(X, x_dtype, M, K, xq, sx, stream):
+    _check(_lib.lbq_quantize_int8_rows(X, x_dtype, M, K, xq, sx, stream))
+
+
+def lbq_quantize_int8_weight(W, K, N, wq, sw, stream):
+    _check(_lib.lbq_quantize_int8_weight(W, K, N, wq, sw, stream))
+
+
+def lbq_w8a8_gemm(xq, sx, M, K, N, wq, sw, Y, y_dtype, stream):
+    _check(_lib.lbq_w8a8_gemm(xq, sx, M, K, N, wq, sw, Y, y_dtype, stream))
+
+
+def lbq_w8a8_workspace_size(M, K):
+    n = _c_size(0)
+    _check(_lib.lbq_w8a8_workspace_size(M, K, ctypes.byref(n)))
+    return n.value
+
+
+def lbq_w8a8_linear(X, x_dtype, M, K, N, wq, sw, Y, y_dtype, ws, ws_bytes, stream):
+    _check(_lib.lbq_w8a8_linear(X, x_dtype, M, K, N, wq, sw, Y, y_dtype, ws, ws_bytes, stream))
+
+
+def lbq_moe_w8a8_gemm(xq, sx, rows, K, N, offsets, num_experts, wq, sw, Y, y_dtype, stream):
+    _check(_lib.lbq_moe_w8a8_gemm(xq, sx, rows, K, N, offsets, num_experts, wq, sw, Y, y_dtype, stream))
+
+
+def lbq_moe_sort(topk_ids, num_pairs, num_experts, row_of_pair, pair_of_row, offsets, stream):
+    _check(_lib.lbq_moe_sort(topk_ids, num_pairs, num_experts, row_of_pair, pair_of_row, offsets, stream))
+
+
+def lbq_moe_permute(X, row_bytes, T, top_k, row_of_pair, rows, Xs, stream):
+    _check(_lib.lbq_moe_permute(X, row_bytes, T, top_k, row_of_pair, rows, Xs, stream))
+
+
+def lbq_moe_combine(Ys, dtype, rows, H, row_of_pair, weights, T, top_k, out, stream):
+    _check(_lib.lbq_moe_combine(Ys, dtype, rows, H, row_of_pair, weights, T, top_k, out, stream))
+
+
+def lbq_moe_combine_grad(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, stream):
+    _check(_lib.lbq_moe_combine_grad(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, stream))
 
 
 def lbq_set_option(option, value):
@@ -654,6 +706,178 @@ def moe_lut3_mx_gemm(codes, scales, top_k, aligned, images, stride, num_local_ex
                          expert_ids.data_ptr(), total.data_ptr(), sorted_ids.numel(), images.data_ptr(), stride,
                          num_local_experts, Y.data_ptr(), _dt(Y), _stream())
     return Y
+
+
+def _arg(t, name, dtype, shape):
+    """Check a tensor argument: CUDA, on the current device, contiguous, of this dtype and shape
+    (a dimension None is free)."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.get_device() != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is another: calls run on the "
+                         "current device's stream")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if len(t.shape) != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have the shape {list(shape)} (None: any size), got {list(t.shape)}")
+
+
+def _out_arg(t, name, dtype, shape, device):
+    """An output tensor: the given one, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _arg(t, name, dtype, shape)
+    return t
+
+
+def _y_dtype(y_dtype):
+    torch = _torch()
+    return {"f16": torch.float16, "bf16": torch.bfloat16}.get(y_dtype, y_dtype)
+
+
+def quantize_int8_rows(X):
+    """INT8 activations with one scale per row: X [M, K] FP16/BF16 -> (xq int8 [M, K], sx float32 [M])."""
+    torch = _torch()
+    dt = _dt(X)
+    _arg(X, "X", X.dtype, (None, None))
+    M, K = X.shape
+    xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    sx = torch.empty((M,), dtype=torch.float32, device=X.device)
+    lbq_quantize_int8_rows(X.data_ptr(), dt, M, K, xq.data_ptr(), sx.data_ptr(), _stream())
+    return xq, sx
+
+
+def quantize_int8_weight(W):
+    """INT8 weights with one scale per output channel: W float32 [K, N] -> (wq int8 [N, K], sw float32 [N])."""
+    torch = _torch()
+    _arg(W, "W", torch.float32, (None, None))
+    K, N = W.shape
+    wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
+    sw = torch.empty((N,), dtype=torch.float32, device=W.device)
+    lbq_quantize_int8_weight(W.data_ptr(), K, N, wq.data_ptr(), sw.data_ptr(), _stream())
+    return wq, sw
+
+
+def w8a8_gemm(xq, sx, wq, sw, y_dtype="bf16", Y=None):
+    """Y[m, n] = sx[m] sw[n] sum_k xq[m, k] wq[n, k] for int8 xq [M, K] and wq [N, K], float32 sx [M] and sw [N]."""
+    torch = _torch()
+    _arg(xq, "xq", torch.int8, (None, None))
+    M, K = xq.shape
+    _arg(sx, "sx", torch.float32, (M,))
+    _arg(wq, "wq", torch.int8, (None, K))
+    N = wq.shape[0]
+    _arg(sw, "sw", torch.float32, (N,))
+    Y = _out_arg(Y, "Y", _y_dtype(y_dtype) if Y is None else Y.dtype, (M, N), xq.device)
+    lbq_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), _stream())
+    return Y
+
+
+def w8a8_linear(X, wq, sw, y_dtype=None, ws=None, Y=None):
+    """w8a8_gemm on quantize_int8_rows(X), X [M, K] FP16/BF16, in one call; y_dtype defaults to X's dtype.
+    ws: uint8, lbq_w8a8_workspace_size(M, K) bytes (allocated when not given)."""
+    torch = _torch()
+    dt = _dt(X)
+    _arg(X, "X", X.dtype, (None, None))
+    M, K = X.shape
+    _arg(wq, "wq", torch.int8, (None, K))
+    N = wq.shape[0]
+    _arg(sw, "sw", torch.float32, (N,))
+    if Y is None:
+        Y = torch.empty((M, N), dtype=X.dtype if y_dtype is None else _y_dtype(y_dtype), device=X.device)
+    else:
+        _arg(Y, "Y", Y.dtype, (M, N))
+    if ws is None:
+        ws = torch.empty(lbq_w8a8_workspace_size(M, K), dtype=torch.uint8, device=X.device)
+    else:
+        _arg(ws, "ws", torch.uint8, (None,))
+    lbq_w8a8_linear(X.data_ptr(), dt, M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), ws.data_ptr(),
+                    ws.numel(), _stream())
+    return Y
+
+
+def moe_w8a8_gemm(xq, sx, offsets, wq, sw, y_dtype="bf16", Y=None):
+    """The W8A8 product of rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of xq int8 [rows, K] with
+    expert e's wq int8 [E, N, K] and sw float32 [E, N]. Rows in no run are not written."""
+    torch = _torch()
+    _arg(xq, "xq", torch.int8, (None, None))
+    rows, K = xq.shape
+    _arg(sx, "sx", torch.float32, (rows,))
+    _arg(wq, "wq", torch.int8, (None, None, K))
+    E, N = wq.shape[0], wq.shape[1]
+    _arg(sw, "sw", torch.float32, (E, N))
+    _arg(offsets, "offsets", torch.int32, (E + 1,))
+    Y = _out_arg(Y, "Y", _y_dtype(y_dtype) if Y is None else Y.dtype, (rows, N), xq.device)
+    lbq_moe_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), rows, K, N, offsets.data_ptr(), E, wq.data_ptr(), sw.data_ptr(),
+                      Y.data_ptr(), _dt(Y), _stream())
+    return Y
+
+
+def moe_sort(topk_ids, num_experts):
+    """topk_ids int32 [T, top_k] -> (row_of_pair int32 [T, top_k], pair_of_row int32 [T * top_k], offsets int32
+    [num_experts + 1]): the pairs in ascending (expert, pair) order; -1 for pairs whose id is no expert."""
+    torch = _torch()
+    _arg(topk_ids, "topk_ids", torch.int32, (None, None))
+    T, top_k = topk_ids.shape
+    row = torch.empty((T, top_k), dtype=torch.int32, device=topk_ids.device)
+    pair = torch.empty((T * top_k,), dtype=torch.int32, device=topk_ids.device)
+    offsets = torch.empty((max(num_experts, 0) + 1,), dtype=torch.int32, device=topk_ids.device)
+    lbq_moe_sort(topk_ids.data_ptr(), T * top_k, num_experts, row.data_ptr(), pair.data_ptr(), offsets.data_ptr(),
+                 _stream())
+    return row, pair, offsets
+
+
+def moe_permute(X, row_of_pair, Xs=None):
+    """Xs[row_of_pair[t, j]] = X[t] for X [T, H] of any dtype; Xs [rows, H], by default T * top_k rows. Rows that no
+    entry names (there are such when pairs were dropped) are not written."""
+    torch = _torch()
+    _arg(X, "X", X.dtype, (None, None))
+    T, H = X.shape
+    _arg(row_of_pair, "row_of_pair", torch.int32, (T, None))
+    top_k = row_of_pair.shape[1]
+    Xs = _out_arg(Xs, "Xs", X.dtype, (T * top_k if Xs is None else None, H), X.device)
+    lbq_moe_permute(X.data_ptr(), H * X.element_size(), T, top_k, row_of_pair.data_ptr(), Xs.shape[0], Xs.data_ptr(),
+                    _stream())
+    return Xs
+
+
+def moe_combine(Ys, row_of_pair, weights=None, out=None):
+    """out[t] = sum_j weights[t, j] Ys[row_of_pair[t, j]] (FP32, rounded once) for Ys [rows, H] FP16/BF16 and float32
+    weights [T, top_k] (None: 1); entries of row_of_pair outside the rows add nothing."""
+    torch = _torch()
+    dt = _dt(Ys)
+    _arg(Ys, "Ys", Ys.dtype, (None, None))
+    rows, H = Ys.shape
+    _arg(row_of_pair, "row_of_pair", torch.int32, (None, None))
+    T, top_k = row_of_pair.shape
+    if weights is not None:
+        _arg(weights, "weights", torch.float32, (T, top_k))
+    out = _out_arg(out, "out", Ys.dtype, (T, H), Ys.device)
+    lbq_moe_combine(Ys.data_ptr(), dt, rows, H, row_of_pair.data_ptr(),
+                    weights.data_ptr() if weights is not None else None, T, top_k, out.data_ptr(), _stream())
+    return out
+
+
+def moe_combine_grad(dout, Ys, row_of_pair, weights, dYs=None):
+    """Gradients of moe_combine: (dYs [rows, H], dweights float32 [T, top_k]). Rows of dYs that no entry names are
+    not written."""
+    torch = _torch()
+    dt = _dt(Ys)
+    _arg(Ys, "Ys", Ys.dtype, (None, None))
+    rows, H = Ys.shape
+    _arg(row_of_pair, "row_of_pair", torch.int32, (None, None))
+    T, top_k = row_of_pair.shape
+    _arg(dout, "dout", Ys.dtype, (T, H))
+    _arg(weights, "weights", torch.float32, (T, top_k))
+    dYs = _out_arg(dYs, "dYs", Ys.dtype, (rows, H), Ys.device)
+    dweights = torch.empty((T, top_k), dtype=torch.float32, device=Ys.device)
+    lbq_moe_combine_grad(dout.data_ptr(), Ys.data_ptr(), dt, rows, H, row_of_pair.data_ptr(), weights.data_ptr(), T,
+                         top_k, dYs.data_ptr(), dweights.data_ptr(), _stream())
+    return dYs, dweights
+
+
+def moe_permute_grad(dXs, row_of_pair, dX=None):
+    """Gradient of moe_permute: dX[t] = sum_j dXs[row_of_pair[t, j]] (FP32, rounded once), dXs [rows, H] FP16/BF16."""
+    return moe_combine(dXs, row_of_pair, None, dX)
 
 
 def device_status():

@@ -37,6 +37,8 @@
 #include "affine.cuh"
 #include "w4a8.cuh"
 #include "gemm_moe.cuh"
+#include "w8a8.cuh"
+#include "moe_rows.cuh"
 
 namespace lbq {
 
@@ -1426,6 +1428,153 @@ static uint8_t* noalloc_scratch(cudaStream_t stream, lbq_status* st) {
   return ptr[dev];
 }
 
+// ----------------------------------------------------------------------------
+// W8A8: dense and routed products
+// ----------------------------------------------------------------------------
+
+struct W8Plan {
+  int ht, n_tiles, bn, m_tiles, bx, grid;
+};
+
+// Shape of the tiles: token tiles of bn <= 256 rows, channel tiles of ht <= 128
+// rows. Few tokens: the weights' bytes are the time, and ht is cut so that the
+// tiles fill whole waves of SMs (any height works: the TMA box has ht rows).
+// Many tokens: the MMA time of a tile does not fall with ht, so ht stays 128
+// and bn is cut instead. One cost decides: waves x k-blocks x the longer of the
+// MMA time and the operand loads of a tile, and never below the weights' HBM time.
+static W8Plan plan_w8a8(long long M, int K, int N) {
+  const int sms = num_sms();
+  const int nkb = (K + kW8BK - 1) / kW8BK;
+  W8Plan best{};
+  double best_cost = 0.0;
+  const long long m_min = (M + kW8MaxBn - 1) / kW8MaxBn;
+  for (long long mt = m_min; mt <= m_min + m_min / 2 + 1; ++mt) {
+    const int bn = (int)((((M + mt - 1) / mt) + 15) / 16 * 16);
+    const long long m_tiles = (M + bn - 1) / bn;
+    const long long w0 = ((N + kW8MaxHt - 1) / kW8MaxHt * m_tiles + sms - 1) / sms;
+    for (long long w = w0; w <= w0 + 1; ++w) {
+      const long long nt = std::max<long long>(1, std::min<long long>(N, w * sms / m_tiles));
+      int ht = (int)std::min<long long>(kW8MaxHt, (N + nt - 1) / nt);
+      for (int full = 0; full < 2; ++full) {
+        if (full) ht = std::min(kW8MaxHt, N);
+        const long long tiles = (N + ht - 1) / ht * m_tiles;
+        const double waves = (double)((tiles + sms - 1) / sms);
+        const double mma = std::max(2.0 * bn, 128.0 + bn);    // cycles per k-block: rate, shared-memory reads
+        const double load = (ht + bn) * 128.0 / 48.0;         // cycles per k-block at 48 B per cycle and SM
+        const double cost = waves * (nkb * std::max(mma, load) + 600.0);
+        if (best.bn == 0 || cost < best_cost) {
+          best_cost = cost;
+          best.ht = ht;
+          best.n_tiles = (N + ht - 1) / ht;
+          best.bn = bn;
+          best.m_tiles = (int)m_tiles;
+          best.bx = bn;
+          best.grid = (int)std::min<long long>(tiles, sms);
+        }
+      }
+    }
+  }
+  return best;
+}
+
+// Routed: the rows of each expert are known on the device only, so the tile is
+// chosen for the mean run of an expert.
+static W8Plan plan_moe_w8a8(int M, int N, int E) {
+  W8Plan p{};
+  const int mean = (M + E - 1) / E;
+  p.bn = mean <= 8 ? 16 : mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 90 ? 128 : 256;
+  p.bx = std::min(p.bn, 32);
+  p.ht = std::min(kW8MaxHt, N);
+  p.n_tiles = (N + p.ht - 1) / p.ht;
+  p.m_tiles = 0;
+  p.grid = (int)std::min<long long>((long long)p.n_tiles * ((long long)M / p.bn + std::min(E, M)), num_sms());
+  return p;
+}
+
+static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int N, int E, const int32_t* offsets,
+                           const int8_t* wq, const float* sw, void* Y, bool ybf16, bool pdl, cudaStream_t st) {
+  const W8Plan p = offsets ? plan_moe_w8a8(M, N, E) : plan_w8a8(M, K, N);
+  CUtensorMap tw, tx;
+  if (!make_tmap_2d(&tw, wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K, (uint64_t)E * (uint64_t)N, (uint64_t)K,
+                    kW8BK, (uint32_t)p.ht, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K, (uint64_t)M, (uint64_t)K, kW8BK,
+                    (uint32_t)p.bx, CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(LBQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the W8A8 operands");
+  W8a8Args a{};
+  a.Y = Y;
+  a.sx = sx;
+  a.sw = sw;
+  a.offsets = offsets;
+  a.M = M; a.N = N; a.E = E;
+  a.ht = p.ht; a.n_tiles = p.n_tiles;
+  a.bn = p.bn; a.m_tiles = p.m_tiles; a.bx = p.bx;
+  a.k_blocks = (K + kW8BK - 1) / kW8BK;
+  a.a_bytes = (int)align_up((size_t)p.ht, 8) * kW8BK;
+  a.stage_bytes = a.a_bytes + p.bn * kW8BK;
+  a.acc_stride = (int)align_up((size_t)p.bn, 32);
+  a.tmem_cols = 64;
+  while (a.tmem_cols < 2 * a.acc_stride) a.tmem_cols *= 2;
+  a.y_bf16 = ybf16 ? 1 : 0;
+  // alignment, the slack behind the ring, and the routed form's tile counts
+  const int extra = 1024 + kW8MaxHt * kW8BK + (offsets ? (E + 1) * (int)sizeof(int) : 0);
+  a.stages = std::min(kW8MaxStages, (kW8SmemBudget - extra) / a.stage_bytes);
+  const int smem = a.stages * a.stage_bytes + extra;
+  const void* fn = (const void*)w8a8_gemm_kernel;
+  occupancy_for(fn, kW8Threads, smem);
+  void* args[] = {&tw, &tx, &a};
+  return launch_kernel_ex(fn, dim3(p.grid), dim3(kW8Threads), smem, st, pdl, args, "W8A8 GEMM launch");
+}
+
+static lbq_status run_quantize_rows(const void* X, int x_dtype, int M, int K, int8_t* xq, float* sx, cudaStream_t st) {
+  const int chunks = K / 8;
+  const int vpt = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
+  const int block = std::max(32, (int)align_up((size_t)((chunks + vpt - 1) / vpt), 32));
+  const bool b = x_dtype == LBQ_DTYPE_BF16;
+  const void* fn = vpt == 1   ? (b ? (const void*)quantize_int8_rows_kernel<true, 1> : (const void*)quantize_int8_rows_kernel<false, 1>)
+                   : vpt == 2 ? (b ? (const void*)quantize_int8_rows_kernel<true, 2> : (const void*)quantize_int8_rows_kernel<false, 2>)
+                   : vpt == 4 ? (b ? (const void*)quantize_int8_rows_kernel<true, 4> : (const void*)quantize_int8_rows_kernel<false, 4>)
+                              : (b ? (const void*)quantize_int8_rows_kernel<true, 8> : (const void*)quantize_int8_rows_kernel<false, 8>);
+  const uint16_t* Xp = static_cast<const uint16_t*>(X);
+  void* args[] = {(void*)&Xp, (void*)&K, (void*)&xq, (void*)&sx};
+  return launch_kernel_ex(fn, dim3((unsigned)M), dim3(block), 0, st, g_pdl != 0, args, "quantize_int8_rows launch");
+}
+
+static lbq_status check_w8a8_shape(int M, int K, int N) {
+  if (M <= 0 || K <= 0 || N <= 0) return fail(LBQ_ERR_INVALID_ARG, "M=%d K=%d N=%d must be positive", M, K, N);
+  if (K % 16) return fail(LBQ_ERR_INVALID_ARG, "K=%d is not a multiple of 16", K);
+  if (K > kW8MaxK) return fail(LBQ_ERR_UNSUPPORTED, "K=%d > %d", K, kW8MaxK);
+  return LBQ_OK;
+}
+
+// What the products read and write besides the activations.
+static lbq_status check_w8a8_weights(const void* wq, const void* sw, const void* Y, int y_dtype) {
+  if (!wq || !sw || !Y) return fail(LBQ_ERR_INVALID_ARG, "wq, sw and Y must be non-null");
+  if (!aligned16(wq) || !aligned16(sw) || !aligned16(Y))
+    return fail(LBQ_ERR_INVALID_ARG, "wq, sw and Y must be 16-byte aligned");
+  if (y_dtype != LBQ_DTYPE_F16 && y_dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "y_dtype %d", y_dtype);
+  return LBQ_OK;
+}
+
+// ----------------------------------------------------------------------------
+// Rows of routed tokens
+// ----------------------------------------------------------------------------
+
+// Sizes shared by the row calls: T tokens of top_k choices, `rows` sorted rows.
+static lbq_status check_routed(int T, int top_k, int rows) {
+  if (T <= 0 || top_k <= 0 || rows <= 0)
+    return fail(LBQ_ERR_INVALID_ARG, "T=%d top_k=%d rows=%d must be positive", T, top_k, rows);
+  if ((long long)T * top_k >= (1LL << 30)) return fail(LBQ_ERR_INVALID_ARG, "T * top_k too large");
+  return LBQ_OK;
+}
+
+// Blocks of 256 threads over `pieces` row pieces.
+static lbq_status pieces_grid(long long pieces, unsigned* grid) {
+  const long long g = (pieces + 255) / 256;
+  if (g > 0x7FFFFFFFLL) return fail(LBQ_ERR_INVALID_ARG, "too many elements for one launch");
+  *grid = (unsigned)g;
+  return LBQ_OK;
+}
+
 }  // namespace lbq
 
 using namespace lbq;
@@ -2025,6 +2174,171 @@ lbq_status lbq_moe_lut3_mx_gemm(const uint8_t* codes, const uint8_t* scales, int
   void* args[] = {&a};
   return launch_kernel_ex(fn, dim3(grid), dim3(kMoeThreads), smem, static_cast<cudaStream_t>(stream), false, args,
                           "MoE LUT3 x MXFP8 GEMM launch");
+}
+
+lbq_status lbq_quantize_int8_rows(const void* X, int x_dtype, int M, int K, int8_t* xq, float* sx, void* stream) {
+  if (!X || !xq || !sx) return fail(LBQ_ERR_INVALID_ARG, "X, xq and sx must be non-null");
+  if (!aligned16(X) || !aligned16(xq) || !aligned16(sx))
+    return fail(LBQ_ERR_INVALID_ARG, "X, xq and sx must be 16-byte aligned");
+  if (x_dtype != LBQ_DTYPE_F16 && x_dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "x_dtype %d", x_dtype);
+  lbq_status st = check_w8a8_shape(M, K, 1);
+  if (st != LBQ_OK) return st;
+  return run_quantize_rows(X, x_dtype, M, K, xq, sx, static_cast<cudaStream_t>(stream));
+}
+
+lbq_status lbq_quantize_int8_weight(const float* W, int K, int N, int8_t* wq, float* sw, void* stream) {
+  if (!W || !wq || !sw) return fail(LBQ_ERR_INVALID_ARG, "W, wq and sw must be non-null");
+  if (!aligned16(W) || !aligned16(wq) || !aligned16(sw))
+    return fail(LBQ_ERR_INVALID_ARG, "W, wq and sw must be 16-byte aligned");
+  lbq_status st = check_w8a8_shape(1, K, N);
+  if (st != LBQ_OK) return st;
+  void* args[] = {(void*)&W, (void*)&K, (void*)&N, (void*)&wq, (void*)&sw};
+  return launch_kernel_ex((const void*)quantize_int8_weight_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0,
+                          static_cast<cudaStream_t>(stream), false, args, "quantize_int8_weight launch");
+}
+
+lbq_status lbq_w8a8_gemm(const int8_t* xq, const float* sx, int M, int K, int N, const int8_t* wq, const float* sw,
+                         void* Y, int y_dtype, void* stream) {
+  lbq_status st = check_w8a8_shape(M, K, N);
+  if (st != LBQ_OK) return st;
+  if (!xq || !sx) return fail(LBQ_ERR_INVALID_ARG, "xq and sx must be non-null");
+  if (!aligned16(xq) || !aligned16(sx)) return fail(LBQ_ERR_INVALID_ARG, "xq and sx must be 16-byte aligned");
+  if ((st = check_w8a8_weights(wq, sw, Y, y_dtype)) != LBQ_OK) return st;
+  return run_w8a8(xq, sx, M, K, N, 1, nullptr, wq, sw, Y, y_dtype == LBQ_DTYPE_BF16, g_pdl != 0,
+                  static_cast<cudaStream_t>(stream));
+}
+
+lbq_status lbq_w8a8_workspace_size(int M, int K, size_t* bytes) {
+  if (!bytes) return fail(LBQ_ERR_INVALID_ARG, "bytes must be non-null");
+  lbq_status st = check_w8a8_shape(M, K, 1);
+  if (st != LBQ_OK) return st;
+  *bytes = align_up((size_t)M * K, 256) + align_up((size_t)M * sizeof(float), 256);
+  return LBQ_OK;
+}
+
+lbq_status lbq_w8a8_linear(const void* X, int x_dtype, int M, int K, int N, const int8_t* wq, const float* sw, void* Y,
+                           int y_dtype, void* ws, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  lbq_status st = check_w8a8_shape(M, K, N);
+  if (st != LBQ_OK) return st;
+  if ((st = lbq_w8a8_workspace_size(M, K, &need)) != LBQ_OK) return st;
+  if (!X || !ws) return fail(LBQ_ERR_INVALID_ARG, "X and ws must be non-null");
+  if (!aligned16(X) || !aligned16(ws)) return fail(LBQ_ERR_INVALID_ARG, "X and ws must be 16-byte aligned");
+  if (x_dtype != LBQ_DTYPE_F16 && x_dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "x_dtype %d", x_dtype);
+  if (ws_bytes < need) return fail(LBQ_ERR_INVALID_ARG, "workspace of %zu bytes is too small (need %zu)", ws_bytes, need);
+  if ((st = check_w8a8_weights(wq, sw, Y, y_dtype)) != LBQ_OK) return st;
+  int8_t* xq = static_cast<int8_t*>(ws);
+  float* sx = reinterpret_cast<float*>(xq + align_up((size_t)M * K, 256));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = run_quantize_rows(X, x_dtype, M, K, xq, sx, s)) != LBQ_OK) return st;
+  // the product may start (and fetch weights) while the activations are quantised
+  return run_w8a8(xq, sx, M, K, N, 1, nullptr, wq, sw, Y, y_dtype == LBQ_DTYPE_BF16, true, s);
+}
+
+lbq_status lbq_moe_w8a8_gemm(const int8_t* xq, const float* sx, int rows, int K, int N, const int32_t* offsets,
+                             int num_experts, const int8_t* wq, const float* sw, void* Y, int y_dtype, void* stream) {
+  lbq_status st = check_w8a8_shape(rows, K, N);
+  if (st != LBQ_OK) return st;
+  if (num_experts <= 0 || num_experts > kW8MaxExperts)
+    return fail(LBQ_ERR_INVALID_ARG, "num_experts=%d not in 1..%d", num_experts, kW8MaxExperts);
+  if ((long long)num_experts * N > 0x7FFFFFFFLL) return fail(LBQ_ERR_INVALID_ARG, "num_experts * N too large");
+  if (!xq || !sx || !offsets) return fail(LBQ_ERR_INVALID_ARG, "xq, sx and offsets must be non-null");
+  if (!aligned16(xq) || !aligned16(sx) || !aligned16(offsets))
+    return fail(LBQ_ERR_INVALID_ARG, "xq, sx and offsets must be 16-byte aligned");
+  if ((st = check_w8a8_weights(wq, sw, Y, y_dtype)) != LBQ_OK) return st;
+  return run_w8a8(xq, sx, rows, K, N, num_experts, offsets, wq, sw, Y, y_dtype == LBQ_DTYPE_BF16, g_pdl != 0,
+                  static_cast<cudaStream_t>(stream));
+}
+
+lbq_status lbq_moe_sort(const int32_t* topk_ids, int num_pairs, int num_experts, int32_t* row_of_pair,
+                        int32_t* pair_of_row, int32_t* offsets, void* stream) {
+  if (!topk_ids || !row_of_pair || !pair_of_row || !offsets)
+    return fail(LBQ_ERR_INVALID_ARG, "topk_ids, row_of_pair, pair_of_row and offsets must be non-null");
+  if (!aligned16(topk_ids) || !aligned16(row_of_pair) || !aligned16(pair_of_row) || !aligned16(offsets))
+    return fail(LBQ_ERR_INVALID_ARG, "topk_ids, row_of_pair, pair_of_row and offsets must be 16-byte aligned");
+  if (num_pairs <= 0 || num_pairs >= (1 << 30) || num_experts <= 0 || num_experts > kW8MaxExperts)
+    return fail(LBQ_ERR_INVALID_ARG, "num_pairs=%d (below 2^30) num_experts=%d (1..%d)", num_pairs, num_experts,
+                kW8MaxExperts);
+  const int block = std::min(kSortThreads, std::max(32, (int)align_up((size_t)std::min(num_pairs, kSortThreads), 32)));
+  void* args[] = {(void*)&topk_ids, (void*)&num_pairs, (void*)&num_experts, (void*)&row_of_pair, (void*)&pair_of_row,
+                  (void*)&offsets};
+  return launch_kernel_ex((const void*)moe_sort_kernel, dim3((unsigned)num_experts), dim3(block), 0,
+                          static_cast<cudaStream_t>(stream), g_pdl != 0, args, "MoE sort launch");
+}
+
+lbq_status lbq_moe_permute(const void* X, int row_bytes, int T, int top_k, const int32_t* row_of_pair, int rows,
+                           void* Xs, void* stream) {
+  lbq_status st = check_routed(T, top_k, rows);
+  if (st != LBQ_OK) return st;
+  if (row_bytes <= 0) return fail(LBQ_ERR_INVALID_ARG, "row_bytes=%d must be positive", row_bytes);
+  if (!X || !row_of_pair || !Xs) return fail(LBQ_ERR_INVALID_ARG, "X, row_of_pair and Xs must be non-null");
+  if (!aligned16(X) || !aligned16(row_of_pair) || !aligned16(Xs))
+    return fail(LBQ_ERR_INVALID_ARG, "X, row_of_pair and Xs must be 16-byte aligned");
+  const int b = row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : row_bytes % 2 == 0 ? 2 : 1;
+  const void* fn = b == 16  ? (const void*)moe_permute_kernel<16>
+                   : b == 8 ? (const void*)moe_permute_kernel<8>
+                   : b == 4 ? (const void*)moe_permute_kernel<4>
+                   : b == 2 ? (const void*)moe_permute_kernel<2>
+                            : (const void*)moe_permute_kernel<1>;
+  int per_row = row_bytes / b;
+  long long pieces = (long long)T * per_row;
+  unsigned grid = 0;
+  if ((st = pieces_grid(pieces, &grid)) != LBQ_OK) return st;
+  void* args[] = {(void*)&X, (void*)&pieces, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair, (void*)&rows,
+                  (void*)&Xs};
+  return launch_kernel_ex(fn, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
+                          "MoE permute launch");
+}
+
+lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int32_t* row_of_pair,
+                           const float* weights, int T, int top_k, void* out, void* stream) {
+  lbq_status st = check_routed(T, top_k, rows);
+  if (st != LBQ_OK) return st;
+  if (H <= 0) return fail(LBQ_ERR_INVALID_ARG, "H=%d must be positive", H);
+  if (dtype != LBQ_DTYPE_F16 && dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if (!Ys || !row_of_pair || !out) return fail(LBQ_ERR_INVALID_ARG, "Ys, row_of_pair and out must be non-null");
+  if (!aligned16(Ys) || !aligned16(row_of_pair) || !aligned16(out) || !aligned16(weights))
+    return fail(LBQ_ERR_INVALID_ARG, "Ys, row_of_pair, weights and out must be 16-byte aligned");
+  const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
+  const bool b = dtype == LBQ_DTYPE_BF16;
+  const void* fn = n == 8   ? (b ? (const void*)moe_combine_kernel<true, 8> : (const void*)moe_combine_kernel<false, 8>)
+                   : n == 4 ? (b ? (const void*)moe_combine_kernel<true, 4> : (const void*)moe_combine_kernel<false, 4>)
+                   : n == 2 ? (b ? (const void*)moe_combine_kernel<true, 2> : (const void*)moe_combine_kernel<false, 2>)
+                            : (b ? (const void*)moe_combine_kernel<true, 1> : (const void*)moe_combine_kernel<false, 1>);
+  int per_row = H / n;
+  long long pieces = (long long)T * per_row;
+  unsigned grid = 0;
+  if ((st = pieces_grid(pieces, &grid)) != LBQ_OK) return st;
+  void* args[] = {(void*)&Ys, (void*)&rows, (void*)&pieces, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
+                  (void*)&weights, (void*)&out};
+  return launch_kernel_ex(fn, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
+                          "MoE combine launch");
+}
+
+lbq_status lbq_moe_combine_grad(const void* dout, const void* Ys, int dtype, int rows, int H,
+                                const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
+                                float* dweights, void* stream) {
+  lbq_status st = check_routed(T, top_k, rows);
+  if (st != LBQ_OK) return st;
+  if (H <= 0) return fail(LBQ_ERR_INVALID_ARG, "H=%d must be positive", H);
+  if (dtype != LBQ_DTYPE_F16 && dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if (!dout || !Ys || !row_of_pair || !weights || !dYs || !dweights)
+    return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be non-null");
+  if (!aligned16(dout) || !aligned16(Ys) || !aligned16(row_of_pair) || !aligned16(weights) || !aligned16(dYs) ||
+      !aligned16(dweights))
+    return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be 16-byte aligned");
+  const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
+  const bool b = dtype == LBQ_DTYPE_BF16;
+  const void* fn = n == 8   ? (b ? (const void*)moe_combine_grad_kernel<true, 8> : (const void*)moe_combine_grad_kernel<false, 8>)
+                   : n == 4 ? (b ? (const void*)moe_combine_grad_kernel<true, 4> : (const void*)moe_combine_grad_kernel<false, 4>)
+                   : n == 2 ? (b ? (const void*)moe_combine_grad_kernel<true, 2> : (const void*)moe_combine_grad_kernel<false, 2>)
+                            : (b ? (const void*)moe_combine_grad_kernel<true, 1> : (const void*)moe_combine_grad_kernel<false, 1>);
+  int per_row = H / n;
+  const int block = std::min(256, std::max(32, (int)align_up((size_t)per_row, 32)));
+  void* args[] = {(void*)&dout, (void*)&Ys, (void*)&rows, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
+                  (void*)&weights, (void*)&dYs, (void*)&dweights};
+  return launch_kernel_ex(fn, dim3((unsigned)T), dim3(block), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
+                          "MoE combine gradient launch");
 }
 
 }  // extern "C"

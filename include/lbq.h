@@ -509,6 +509,131 @@ lbq_status lbq_moe_lut3_mx_gemm(const uint8_t* codes, const uint8_t* scales, int
                                 int max_padded, const void* images, size_t image_stride, int num_local_experts,
                                 void* Y, int y_dtype, void* stream);
 
+/*
+ * W8A8: INT8 weights with one FP32 scale per output channel times INT8
+ * activations with one FP32 scale per token, the integer sum exact in int32:
+ *   Y[m][n] = sx[m] sw[n] sum_k xq[m][k] wq[n][k]
+ * The codes of both operands lie with k contiguous (activations [M, K], weights
+ * [N, K]); that is the layout the kernels read, so there is no packed image.
+ * Codes are any int8 value (-128 too). K % 16 == 0, K <= 65536.
+ *
+ * lbq_quantize_int8_rows: dynamic activations, one scale per row of X, in IEEE FP32:
+ *   s = amax / 127 (amax the row's largest |x|);
+ *   xq = clamp(rint(x / s), -127, 127), ties to even; a row of zeros has s = 0
+ *   and xq = 0. A row that holds a NaN or an infinity has that as its scale and
+ *   xq = 0, so its products are NaN.
+ *   X   (device) [M, K] row-major, x_dtype (LBQ_DTYPE_F16 / BF16)
+ *   xq  (device) int8 [M, K];  sx (device) float32 [M]
+ * It also serves weights that are stored [N, K] in FP16 or BF16.
+ * Errors: LBQ_ERR_INVALID_ARG for null or misaligned pointers or bad sizes,
+ * LBQ_ERR_UNSUPPORTED for an unknown x_dtype or K > 65536, before any launch.
+ * Asynchronous on `stream`.
+ */
+lbq_status lbq_quantize_int8_rows(const void* X, int x_dtype, int M, int K, int8_t* xq, float* sx, void* stream);
+
+/*
+ * Quantise an FP32 weight for W8A8 by the same rule, one scale per output channel.
+ *   W   (device) float32 [K, N] row-major, the logical weight of Y = X . W
+ *   wq  (device) int8 [N, K];  sw (device) float32 [N]
+ * Errors as lbq_quantize_int8_rows. Asynchronous on `stream`.
+ */
+lbq_status lbq_quantize_int8_weight(const float* W, int K, int N, int8_t* wq, float* sw, void* stream);
+
+/*
+ * The W8A8 product, any M >= 1, on tcgen05.mma.kind::i8. The int32 sum is
+ * converted to FP32 (rounded above 2^24), multiplied by sw[n], then by sx[m],
+ * and rounded to nearest in y_dtype; results do not depend on M or the tiling.
+ *   xq, sx (device) from lbq_quantize_int8_rows (or any codes and scales)
+ *   wq, sw (device) int8 [N, K] codes, float32 [N] scales
+ *   Y      (device) [M, N] row-major, y_dtype, fully overwritten
+ * No workspace. Errors: LBQ_ERR_INVALID_ARG for null or misaligned pointers or
+ * bad sizes, LBQ_ERR_UNSUPPORTED for K > 65536 or an unknown y_dtype, before
+ * any launch. Asynchronous on `stream`.
+ */
+lbq_status lbq_w8a8_gemm(const int8_t* xq, const float* sx, int M, int K, int N, const int8_t* wq, const float* sw,
+                         void* Y, int y_dtype, void* stream);
+
+/*
+ * lbq_quantize_int8_rows followed by lbq_w8a8_gemm (the same results), with the
+ * product's weight loads under way while the activations are quantised; the
+ * weights must not be written by kernels of the same stream that may still run.
+ *   ws (device) lbq_w8a8_workspace_size(M, K) bytes, contents free; it holds the
+ *      codes and scales, so calls that may run at the same time need one each
+ * lbq_w8a8_workspace_size writes *bytes (host); no device work. Errors as the
+ * two calls, and LBQ_ERR_INVALID_ARG for a workspace that is too small.
+ */
+lbq_status lbq_w8a8_workspace_size(int M, int K, size_t* bytes);
+lbq_status lbq_w8a8_linear(const void* X, int x_dtype, int M, int K, int N, const int8_t* wq, const float* sw, void* Y,
+                           int y_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The routed W8A8 product: rows sorted by expert, one weight per expert.
+ *   Y[r][n] = sx[r] sw[e][n] sum_k xq[r][k] wq[e][n][k]
+ * for the expert e with offsets[e] <= r < offsets[e + 1].
+ *   xq, sx  (device) int8 [rows, K], float32 [rows]
+ *   offsets (device) int32 [num_experts + 1], not decreasing (lbq_moe_sort); read on
+ *           the device, values outside 0 .. rows are clamped to it
+ *   wq, sw  (device) int8 [num_experts, N, K], float32 [num_experts, N]
+ *   Y       (device) [rows, N] row-major, y_dtype; rows in no expert's run are not written
+ * num_experts <= 2048. Errors as lbq_w8a8_gemm. Asynchronous on `stream`.
+ */
+lbq_status lbq_moe_w8a8_gemm(const int8_t* xq, const float* sx, int rows, int K, int N, const int32_t* offsets,
+                             int num_experts, const int8_t* wq, const float* sw, void* Y, int y_dtype, void* stream);
+
+/*
+ * Rows of routed tokens. Pair p = t * top_k + j is token t's j-th choice.
+ *
+ * lbq_moe_sort: the pairs ordered by (expert, p), without padding; the same
+ * input gives the same order.
+ *   topk_ids    (device) int32 [num_pairs]; ids outside 0 .. num_experts - 1 mark
+ *               pairs without an expert here (dropped, or on another rank)
+ *   row_of_pair (device) int32 [num_pairs]: the pair's row in the order, -1 without an expert
+ *   pair_of_row (device) int32 [num_pairs]: the inverse, -1 past the last row
+ *   offsets     (device) int32 [num_experts + 1]: first row of each expert's run; the
+ *               last entry is the number of rows
+ * num_pairs < 2^30, num_experts <= 2048. Errors before any launch:
+ * LBQ_ERR_INVALID_ARG. Asynchronous on `stream`.
+ */
+lbq_status lbq_moe_sort(const int32_t* topk_ids, int num_pairs, int num_experts, int32_t* row_of_pair,
+                        int32_t* pair_of_row, int32_t* offsets, void* stream);
+
+/*
+ * Xs[row_of_pair[t][j]] = X[t] for rows of `row_bytes` bytes of any type (FP16,
+ * BF16, INT8 or E4M3 codes, scales).
+ *   X           (device) [T] rows;  Xs (device) [rows] rows
+ *   row_of_pair (device) int32 [T, top_k], its entries different; entries outside
+ *               0 .. rows - 1 are skipped, rows of Xs that no entry names are not written
+ * Errors before any launch: LBQ_ERR_INVALID_ARG. Asynchronous on `stream`.
+ */
+lbq_status lbq_moe_permute(const void* X, int row_bytes, int T, int top_k, const int32_t* row_of_pair, int rows,
+                           void* Xs, void* stream);
+
+/*
+ * out[t] = sum_j weights[t][j] Ys[row_of_pair[t][j]], in FP32 with j ascending,
+ * rounded once; skipped entries (outside 0 .. rows - 1) add nothing.
+ *   Ys      (device) [rows, H], out (device) [T, H], both `dtype` (LBQ_DTYPE_F16 / BF16)
+ *   weights (device) float32 [T, top_k], or null for 1: that is the gradient of
+ *           lbq_moe_permute, dX[t] = sum_j dXs[row_of_pair[t][j]]
+ * Errors before any launch: LBQ_ERR_INVALID_ARG, LBQ_ERR_UNSUPPORTED for an
+ * unknown dtype. Asynchronous on `stream`.
+ */
+lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int32_t* row_of_pair,
+                           const float* weights, int T, int top_k, void* out, void* stream);
+
+/*
+ * The gradient of lbq_moe_combine:
+ *   dYs[row_of_pair[t][j]] = weights[t][j] dout[t]   (rounded once to dtype)
+ *   dweights[t][j] = sum_h dout[t][h] Ys[row_of_pair[t][j]][h]   (FP32, a fixed order)
+ *   dout (device) [T, H], Ys and dYs (device) [rows, H], `dtype`
+ *   weights, dweights (device) float32 [T, top_k]
+ * The entries of row_of_pair are different; skipped entries have dweights 0, and
+ * rows of dYs that no entry names are not written. dYs may be Ys. Errors as
+ * lbq_moe_combine. Asynchronous on `stream`.
+ */
+lbq_status lbq_moe_combine_grad(const void* dout, const void* Ys, int dtype, int rows, int H,
+                                const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
+                                float* dweights, void* stream);
+
 /* Number of kernel launches the library has enqueued so far in this process. */
 uint64_t lbq_launch_count(void);
 

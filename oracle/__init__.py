@@ -30,6 +30,10 @@ What it computes, and where each step comes from:
   activations: moe_align_block_size (expert-sorted, block-padded pair lists)
   and the gathered product with zero rows for non-local experts (vLLM PR
   62759 write-up, gather and expert-parallelism sections).
+* ``oracle.w8a8``   -- INT8 weights and activations with one scale per channel and
+  per row, dense and routed, from exact integer sums.
+* ``oracle.moe_rows`` -- routed tokens' rows: the stable order by expert, the rows
+  copied into it and combined again, and the gradients.
 * ``oracle.matmul`` -- Y = X . W accumulated in FP64, the error scale
   S = |X| . |W|, and the acceptance test |y - y_ref| <= 4e-3*S + ulp16(|y_ref|).
 
@@ -44,4 +48,4 @@ decoders, nearest-level characterisation of the quantiser). Quantisation
 and it is out of scope.
 """
 
-from . import affine, int4, lut3, matmul, moe, mxfp8, w4a8  # noqa: F401
+from . import affine, int4, lut3, matmul, moe, moe_rows, mxfp8, w4a8, w8a8  # noqa: F401

@@ -1,0 +1,292 @@
+"""W8A8 on the GPU: the quantisers bit for bit, the dense and the routed product against the exact integer sums.
+
+Tolerance of a product, from the roundings it makes: the integer sum to FP32 (half a step, 2^-24 relative), two FP32
+products (2^-24 each) and the output (half a step of its type, and for FP16 half its smallest step, 2^-25)."""
+
+import numpy as np
+import pytest
+
+from oracle import w8a8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    assert torch.cuda.is_available(), "these tests need a CUDA device"
+    return torch
+
+
+@pytest.fixture(scope="module")
+def lbq():
+    import bit_weight_only_pack_b200 as lbq
+    return lbq
+
+
+def codes(rng, shape):
+    return rng.integers(-128, 128, size=shape, dtype=np.int8)
+
+
+def scales(rng, n):
+    return np.exp2(rng.uniform(-12, -8, size=n)).astype(np.float32)
+
+
+def check(torch, Y, ref):
+    y = Y.double().cpu().numpy()
+    u = torch.finfo(Y.dtype).eps / 2
+    tol = np.abs(ref) * ((1 + u) * (1 + 2.0 ** -24) ** 3 - 1) + (2.0 ** -25 if Y.dtype == torch.float16 else 0.0)
+    bad = ~(np.abs(y - ref) <= tol)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outputs off, first at {np.argwhere(bad)[0]}"
+
+
+def cuda(torch, *arrays):
+    return [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in arrays]
+
+
+def guarded(torch, rows, N, dtype):
+    """An output of `rows` rows between two guard rows, and a check that the guards are as they were. (The output
+    starts 16-byte aligned: the guard in front is a whole number of 16-byte pieces.)"""
+    front = 64
+    flat = torch.full((front + rows * N + 64,), 7.0, dtype=dtype, device="cuda")
+
+    def untouched():
+        assert bool((flat[:front] == 7).all()) and bool((flat[front + rows * N:] == 7).all())
+    return flat[front:front + rows * N].view(rows, N), untouched
+
+
+# ---------------------------------------------------------------------------- quantisers
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 48), (33, 256), (5, 4096), (2, 4112), (2, 14336), (1, 32768), (1, 65536)])
+def test_quantize_rows_is_bit_exact(torch, lbq, M, K, dt):
+    rng = np.random.default_rng(M * 7 + K)
+    x = rng.standard_normal((M, K), dtype=np.float32) * np.exp2(rng.uniform(-6, 6, size=(M, 1))).astype(np.float32)
+    if M > 2:
+        x[1] = 0.0
+        x[2] *= 2.0 ** -20  # FP16: subnormals
+    X = torch.from_numpy(x).to(torch.float16 if dt == "f16" else torch.bfloat16)
+    xq, sx = lbq.quantize_int8_rows(X.cuda())
+    rq, rs = w8a8.quantize_rows(X.float().numpy())
+    assert np.array_equal(sx.cpu().numpy(), rs)
+    assert np.array_equal(xq.cpu().numpy(), rq)
+
+
+def test_quantize_rows_ties_go_to_even(torch, lbq):
+    """amax 127 makes the scale exactly 1: every half-integer is a tie."""
+    x = torch.arange(-127, 128).float() / 2  # -63.5 .. 63.5 in halves
+    x = torch.cat([x, torch.tensor([127.0])]).view(1, 256)
+    xq, sx = lbq.quantize_int8_rows(x.half().cuda())
+    assert sx.item() == 1.0
+    assert np.array_equal(xq.cpu().numpy(), np.rint(x.numpy()).astype(np.int8))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_rows_with_nan_or_infinity_have_nan_products(torch, lbq, dt):
+    t = torch.float16 if dt == "f16" else torch.bfloat16
+    x = torch.randn(4, 64).to(t)
+    x[1, 5] = float("nan")
+    x[2, 63] = float("-inf")
+    xq, sx = lbq.quantize_int8_rows(x.cuda())
+    s = sx.cpu().numpy()
+    assert np.isnan(s[1]) and s[2] == np.inf and np.isfinite(s[[0, 3]]).all()
+    assert bool((xq[1:3] == 0).all())
+    wq = torch.ones((8, 64), dtype=torch.int8, device="cuda")
+    y = lbq.w8a8_gemm(xq, sx, wq, torch.ones(8, device="cuda"))
+    assert bool(torch.isnan(y[1:3]).all()) and bool(torch.isfinite(y[[0, 3]]).all())
+
+
+@pytest.mark.parametrize("K,N", [(16, 1), (48, 33), (256, 100), (4112, 7)])
+def test_quantize_weight_is_bit_exact(torch, lbq, K, N):
+    rng = np.random.default_rng(K + N)
+    W = (rng.standard_normal((K, N)) * 0.02).astype(np.float32)
+    W[:, 0] = 0.0
+    if N > 6:
+        W[3, 5] = np.nan
+        W[0, 6] = np.inf
+    wq, sw = lbq.quantize_int8_weight(torch.from_numpy(W).cuda())
+    rq, rs = w8a8.quantize_weight(W)
+    assert np.array_equal(sw.cpu().numpy(), rs, equal_nan=True)
+    assert np.array_equal(wq.cpu().numpy(), rq)
+
+
+# ---------------------------------------------------------------------------- dense product
+
+@pytest.mark.parametrize("ydt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [
+    (1, 16, 1), (1, 4096, 1000), (2, 48, 7), (4, 128, 28), (8, 144, 129), (15, 256, 127), (16, 4112, 1003), (17, 2048, 300),
+    (31, 512, 64), (33, 1024, 200), (64, 640, 513), (100, 400, 4099), (255, 128, 130), (256, 272, 257), (257, 384, 96),
+    (300, 1040, 1003), (513, 256, 2000), (1000, 192, 77), (1025, 64, 3000),
+])
+def test_gemm_matches_the_integer_sums(torch, lbq, M, K, N, ydt):
+    rng = np.random.default_rng(M * 31 + K * 7 + N)
+    xq, wq, sx, sw = codes(rng, (M, K)), codes(rng, (N, K)), scales(rng, M), scales(rng, N)
+    t = torch.float16 if ydt == "f16" else torch.bfloat16
+    Y, untouched = guarded(torch, M, N, t)
+    dxq, dsx, dwq, dsw = cuda(torch, xq, sx, wq, sw)
+    lbq.w8a8_gemm(dxq, dsx, dwq, dsw, Y=Y)
+    torch.cuda.synchronize()
+    lbq.device_status()
+    check(torch, Y, w8a8.matmul(xq, sx, wq, sw))
+    untouched()
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_gemm_largest_sums_stay_exact(torch, lbq, M):
+    """Every product at its largest, 2^14, over the longest K: 2^30."""
+    K, N = 65536, 9
+    xq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    wq = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    wq[1] = 127
+    sx, sw = torch.full((M,), 2.0 ** -20, device="cuda"), torch.ones(N, device="cuda")
+    y = lbq.w8a8_gemm(xq, sx, wq, sw)
+    ref = np.full((M, N), 2.0 ** 10)
+    ref[:, 1] = -128.0 * 127 * K * 2.0 ** -20
+    check(torch, y, ref)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 4096), (16, 8192, 28672), (2048, 4096, 14336)])
+def test_gemm_full_size_sampled(torch, lbq, M, K, N):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    xq = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(M, generator=g, device="cuda") * 1e-2
+    sw = torch.rand(N, generator=g, device="cuda") * 1e-2
+    y = lbq.w8a8_gemm(xq, sx, wq, sw)
+    rng = np.random.default_rng(M)
+    rows = np.unique(np.concatenate([[0, M - 1], rng.integers(0, M, 12)]))
+    cols = np.unique(np.concatenate([[0, N - 1], rng.integers(0, N, 200)]))
+    ref = w8a8.matmul(xq[rows].cpu().numpy(), sx[rows].cpu().numpy(), wq[cols].cpu().numpy(), sw[cols].cpu().numpy())
+    check(torch, y[rows][:, cols], ref)
+    assert torch.equal(y, lbq.w8a8_gemm(xq, sx, wq, sw))
+
+
+def test_rows_do_not_depend_on_the_batch(torch, lbq):
+    """Row m of a product is the same at every M (the sums are integers, the scaling is per element)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    xq = torch.randint(-127, 128, (700, 1024), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (555, 1024), generator=g, device="cuda", dtype=torch.int8)
+    sx, sw = torch.rand(700, generator=g, device="cuda"), torch.rand(555, generator=g, device="cuda") * 1e-3
+    y = lbq.w8a8_gemm(xq, sx, wq, sw)
+    for M in (1, 3, 9, 40, 129, 300):
+        assert torch.equal(y[:M], lbq.w8a8_gemm(xq[:M], sx[:M], wq, sw))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1024), (5, 1040, 333), (7, 14336, 256), (16, 64, 100), (200, 512, 130)])
+def test_linear_is_the_two_calls(torch, lbq, M, K, N, dt):
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.float16 if dt == "f16" else torch.bfloat16)
+    wq, sw = lbq.quantize_int8_weight(torch.randn((K, N), generator=g, device="cuda") * 0.02)
+    xq, sx = lbq.quantize_int8_rows(x)
+    y = lbq.w8a8_linear(x, wq, sw)
+    assert y.dtype == x.dtype and torch.equal(y, lbq.w8a8_gemm(xq, sx, wq, sw, y_dtype=dt))
+
+
+def test_linear_on_other_streams_and_in_graphs(torch, lbq):
+    """A side stream, and two graphs with a workspace each, replayed on new inputs in both orders."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wq, sw = lbq.quantize_int8_weight(torch.randn((2048, 600), generator=g, device="cuda") * 0.02)
+    xs = [torch.randn((M, 2048), generator=g, device="cuda").half() for M in (1, 40)]
+    want = [lbq.w8a8_linear(x, wq, sw) for x in xs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [lbq.w8a8_linear(x, wq, sw) for x in xs]
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graphs, ins, outs = [], [], []
+    for x in xs:
+        xi = torch.zeros_like(x)
+        ws = torch.empty(lbq.lbq_w8a8_workspace_size(*x.shape), dtype=torch.uint8, device="cuda")
+        yo = torch.empty((x.shape[0], 600), dtype=x.dtype, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lbq.w8a8_linear(xi, wq, sw, ws=ws, Y=yo)
+        graphs.append(graph), ins.append(xi), outs.append(yo)
+    for order in ((0, 1), (1, 0)):
+        for i in order:
+            ins[i].copy_(xs[i])
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs))
+    lbq.device_status()
+
+
+def test_chain_with_programmatic_launches(torch, lbq):
+    """Three layers back to back, each reading the last one's output, with overlapping launches allowed."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ws = [lbq.quantize_int8_weight(torch.randn((1024, 1024), generator=g, device="cuda") * 0.03) for _ in range(3)]
+    for M in (1, 12, 300):
+        x = torch.randn((M, 1024), generator=g, device="cuda").bfloat16()
+        want = x
+        for wq, sw in ws:
+            want = lbq.w8a8_linear(want, wq, sw)
+        torch.cuda.synchronize()
+        lbq.lbq_set_option(lbq.LBQ_OPT_PDL, 1)
+        try:
+            for _ in range(5):
+                y = x
+                for wq, sw in ws:
+                    y = lbq.w8a8_linear(y, wq, sw)
+                assert torch.equal(y, want)
+        finally:
+            lbq.lbq_set_option(lbq.LBQ_OPT_PDL, 0)
+
+
+# ---------------------------------------------------------------------------- routed product
+
+def runs(rng, E, rows, kind):
+    if kind == "one":
+        counts = np.zeros(E, dtype=np.int64)
+        counts[E // 2] = rows
+    elif kind == "even":
+        counts = np.full(E, rows // E)
+        counts[:rows - counts.sum()] += 1
+    else:
+        counts = rng.multinomial(rows, rng.dirichlet(np.full(E, 0.3)))
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("ydt", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,E,K,N,kind", [
+    (1, 1, 16, 1, "even"), (1, 256, 128, 40, "one"), (8, 32, 2048, 1024, "uneven"), (128, 256, 256, 100, "uneven"),
+    (100, 3, 144, 129, "uneven"), (300, 4, 512, 128, "one"), (700, 8, 400, 333, "uneven"), (900, 2, 128, 300, "even"),
+    (513, 2048, 64, 24, "uneven"), (1500, 6, 256, 77, "uneven"),
+])
+def test_routed_product(torch, lbq, rows, E, K, N, kind, ydt):
+    rng = np.random.default_rng(rows + E)
+    offsets = runs(rng, E, rows, kind)
+    xq, wq, sx, sw = codes(rng, (rows, K)), codes(rng, (E, N, K)), scales(rng, rows), scales(rng, (E, N))
+    t = torch.float16 if ydt == "f16" else torch.bfloat16
+    Y, untouched = guarded(torch, rows, N, t)
+    dxq, dsx, doff, dwq, dsw = cuda(torch, xq, sx, offsets, wq, sw)
+    lbq.moe_w8a8_gemm(dxq, dsx, doff, dwq, dsw, Y=Y)
+    torch.cuda.synchronize()
+    lbq.device_status()
+    check(torch, Y, w8a8.routed_matmul(xq, sx, offsets, wq, sw))
+    untouched()
+
+
+def test_routed_rows_in_no_run_are_left(torch, lbq):
+    """Rows before the first run and after the last one; all runs empty."""
+    rng = np.random.default_rng(9)
+    rows, E, K, N = 200, 5, 128, 72
+    xq, wq, sx, sw = codes(rng, (rows, K)), codes(rng, (E, N, K)), scales(rng, rows), scales(rng, (E, N))
+    dxq, dsx, dwq, dsw = cuda(torch, xq, sx, wq, sw)
+    for offsets in ([3, 3, 20, 20, 21, 150], [0, 0, 0, 0, 0, 0], [200, 200, 200, 200, 200, 200]):
+        off = np.array(offsets, dtype=np.int32)
+        Y = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        lbq.moe_w8a8_gemm(dxq, dsx, cuda(torch, off)[0], dwq, dsw, Y=Y)
+        ref = w8a8.routed_matmul(xq, sx, off, wq, sw)
+        check(torch, Y, np.where(np.isnan(ref), 7.0, ref))
+
+
+def test_routed_with_one_expert_is_the_dense_product(torch, lbq):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xq = torch.randint(-127, 128, (333, 512), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (1, 200, 512), generator=g, device="cuda", dtype=torch.int8)
+    sx, sw = torch.rand(333, generator=g, device="cuda"), torch.rand((1, 200), generator=g, device="cuda") * 1e-3
+    off = torch.tensor([0, 333], dtype=torch.int32, device="cuda")
+    assert torch.equal(lbq.moe_w8a8_gemm(xq, sx, off, wq, sw), lbq.w8a8_gemm(xq, sx, wq[0], sw[0]))

@@ -708,67 +708,91 @@ def moe_lut3_mx_gemm(codes, scales, top_k, aligned, images, stride, num_local_ex
     return Y
 
 
-def _arg(t, name, dtype, shape):
-    """Check a tensor argument: CUDA, on the current device, contiguous, of this dtype and shape
-    (a dimension None is free)."""
+def _here():
+    """(current device, its current stream as an integer): read once per call."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 3 us less than building a Stream object
+    return dev, raw(dev) if raw is not None else _stream()
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Check a tensor argument: CUDA, on the current device, contiguous, of this dtype and shape."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
+        return
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.get_device() != _torch().cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is another: calls run on the "
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}: calls run on the "
                          "current device's stream")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if len(t.shape) != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have the shape {list(shape)} (None: any size), got {list(t.shape)}")
+    raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
 
 
-def _out_arg(t, name, dtype, shape, device):
+def _dims(t, name, n):
+    """The sizes of an n-dimensional CUDA tensor argument."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {list(shape)}")
+    return shape
+
+
+def _out_arg(t, name, dtype, shape, like, dev):
     """An output tensor: the given one, checked, or a new one."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    _arg(t, name, dtype, shape)
+        return like.new_empty(shape, dtype=dtype)
+    _arg(t, name, dtype, shape, dev)
     return t
 
 
-def _y_dtype(y_dtype):
+def _y_torch_dtype(y_dtype, Y):
+    """The output dtype: the given tensor's, or the named one."""
+    if Y is not None:
+        return Y.dtype
     torch = _torch()
-    return {"f16": torch.float16, "bf16": torch.bfloat16}.get(y_dtype, y_dtype)
+    return torch.bfloat16 if y_dtype == "bf16" else torch.float16 if y_dtype == "f16" else y_dtype
 
 
 def quantize_int8_rows(X):
     """INT8 activations with one scale per row: X [M, K] FP16/BF16 -> (xq int8 [M, K], sx float32 [M])."""
     torch = _torch()
     dt = _dt(X)
-    _arg(X, "X", X.dtype, (None, None))
-    M, K = X.shape
-    xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
-    sx = torch.empty((M,), dtype=torch.float32, device=X.device)
-    lbq_quantize_int8_rows(X.data_ptr(), dt, M, K, xq.data_ptr(), sx.data_ptr(), _stream())
+    M, K = _dims(X, "X", 2)
+    dev, stream = _here()
+    _arg(X, "X", X.dtype, (M, K), dev)
+    xq = X.new_empty((M, K), dtype=torch.int8)
+    sx = X.new_empty((M,), dtype=torch.float32)
+    lbq_quantize_int8_rows(X.data_ptr(), dt, M, K, xq.data_ptr(), sx.data_ptr(), stream)
     return xq, sx
 
 
 def quantize_int8_weight(W):
     """INT8 weights with one scale per output channel: W float32 [K, N] -> (wq int8 [N, K], sw float32 [N])."""
     torch = _torch()
-    _arg(W, "W", torch.float32, (None, None))
-    K, N = W.shape
-    wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
-    sw = torch.empty((N,), dtype=torch.float32, device=W.device)
-    lbq_quantize_int8_weight(W.data_ptr(), K, N, wq.data_ptr(), sw.data_ptr(), _stream())
+    K, N = _dims(W, "W", 2)
+    dev, stream = _here()
+    _arg(W, "W", torch.float32, (K, N), dev)
+    wq = W.new_empty((N, K), dtype=torch.int8)
+    sw = W.new_empty((N,))
+    lbq_quantize_int8_weight(W.data_ptr(), K, N, wq.data_ptr(), sw.data_ptr(), stream)
     return wq, sw
 
 
 def w8a8_gemm(xq, sx, wq, sw, y_dtype="bf16", Y=None):
     """Y[m, n] = sx[m] sw[n] sum_k xq[m, k] wq[n, k] for int8 xq [M, K] and wq [N, K], float32 sx [M] and sw [N]."""
     torch = _torch()
-    _arg(xq, "xq", torch.int8, (None, None))
-    M, K = xq.shape
-    _arg(sx, "sx", torch.float32, (M,))
-    _arg(wq, "wq", torch.int8, (None, K))
-    N = wq.shape[0]
-    _arg(sw, "sw", torch.float32, (N,))
-    Y = _out_arg(Y, "Y", _y_dtype(y_dtype) if Y is None else Y.dtype, (M, N), xq.device)
-    lbq_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), _stream())
+    M, K = _dims(xq, "xq", 2)
+    N = _dims(wq, "wq", 2)[0]
+    dev, stream = _here()
+    _arg(xq, "xq", torch.int8, (M, K), dev)
+    _arg(sx, "sx", torch.float32, (M,), dev)
+    _arg(wq, "wq", torch.int8, (N, K), dev)
+    _arg(sw, "sw", torch.float32, (N,), dev)
+    Y = _out_arg(Y, "Y", _y_torch_dtype(y_dtype, Y), (M, N), xq, dev)
+    lbq_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), stream)
     return Y
 
 
@@ -777,21 +801,19 @@ def w8a8_linear(X, wq, sw, y_dtype=None, ws=None, Y=None):
     ws: uint8, lbq_w8a8_workspace_size(M, K) bytes (allocated when not given)."""
     torch = _torch()
     dt = _dt(X)
-    _arg(X, "X", X.dtype, (None, None))
-    M, K = X.shape
-    _arg(wq, "wq", torch.int8, (None, K))
-    N = wq.shape[0]
-    _arg(sw, "sw", torch.float32, (N,))
-    if Y is None:
-        Y = torch.empty((M, N), dtype=X.dtype if y_dtype is None else _y_dtype(y_dtype), device=X.device)
-    else:
-        _arg(Y, "Y", Y.dtype, (M, N))
+    M, K = _dims(X, "X", 2)
+    N = _dims(wq, "wq", 2)[0]
+    dev, stream = _here()
+    _arg(X, "X", X.dtype, (M, K), dev)
+    _arg(wq, "wq", torch.int8, (N, K), dev)
+    _arg(sw, "sw", torch.float32, (N,), dev)
+    Y = _out_arg(Y, "Y", X.dtype if y_dtype is None and Y is None else _y_torch_dtype(y_dtype, Y), (M, N), X, dev)
     if ws is None:
-        ws = torch.empty(lbq_w8a8_workspace_size(M, K), dtype=torch.uint8, device=X.device)
+        ws = X.new_empty((lbq_w8a8_workspace_size(M, K),), dtype=torch.uint8)
     else:
-        _arg(ws, "ws", torch.uint8, (None,))
+        _arg(ws, "ws", torch.uint8, (ws.numel(),), dev)
     lbq_w8a8_linear(X.data_ptr(), dt, M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), ws.data_ptr(),
-                    ws.numel(), _stream())
+                    ws.numel(), stream)
     return Y
 
 
@@ -799,16 +821,17 @@ def moe_w8a8_gemm(xq, sx, offsets, wq, sw, y_dtype="bf16", Y=None):
     """The W8A8 product of rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of xq int8 [rows, K] with
     expert e's wq int8 [E, N, K] and sw float32 [E, N]. Rows in no run are not written."""
     torch = _torch()
-    _arg(xq, "xq", torch.int8, (None, None))
-    rows, K = xq.shape
-    _arg(sx, "sx", torch.float32, (rows,))
-    _arg(wq, "wq", torch.int8, (None, None, K))
-    E, N = wq.shape[0], wq.shape[1]
-    _arg(sw, "sw", torch.float32, (E, N))
-    _arg(offsets, "offsets", torch.int32, (E + 1,))
-    Y = _out_arg(Y, "Y", _y_dtype(y_dtype) if Y is None else Y.dtype, (rows, N), xq.device)
+    rows, K = _dims(xq, "xq", 2)
+    E, N, _ = _dims(wq, "wq", 3)
+    dev, stream = _here()
+    _arg(xq, "xq", torch.int8, (rows, K), dev)
+    _arg(sx, "sx", torch.float32, (rows,), dev)
+    _arg(wq, "wq", torch.int8, (E, N, K), dev)
+    _arg(sw, "sw", torch.float32, (E, N), dev)
+    _arg(offsets, "offsets", torch.int32, (E + 1,), dev)
+    Y = _out_arg(Y, "Y", _y_torch_dtype(y_dtype, Y), (rows, N), xq, dev)
     lbq_moe_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), rows, K, N, offsets.data_ptr(), E, wq.data_ptr(), sw.data_ptr(),
-                      Y.data_ptr(), _dt(Y), _stream())
+                      Y.data_ptr(), _dt(Y), stream)
     return Y
 
 
@@ -816,13 +839,14 @@ def moe_sort(topk_ids, num_experts):
     """topk_ids int32 [T, top_k] -> (row_of_pair int32 [T, top_k], pair_of_row int32 [T * top_k], offsets int32
     [num_experts + 1]): the pairs in ascending (expert, pair) order; -1 for pairs whose id is no expert."""
     torch = _torch()
-    _arg(topk_ids, "topk_ids", torch.int32, (None, None))
-    T, top_k = topk_ids.shape
-    row = torch.empty((T, top_k), dtype=torch.int32, device=topk_ids.device)
-    pair = torch.empty((T * top_k,), dtype=torch.int32, device=topk_ids.device)
-    offsets = torch.empty((max(num_experts, 0) + 1,), dtype=torch.int32, device=topk_ids.device)
+    T, top_k = _dims(topk_ids, "topk_ids", 2)
+    dev, stream = _here()
+    _arg(topk_ids, "topk_ids", torch.int32, (T, top_k), dev)
+    row = topk_ids.new_empty((T, top_k))
+    pair = topk_ids.new_empty((T * top_k,))
+    offsets = topk_ids.new_empty((max(num_experts, 0) + 1,))
     lbq_moe_sort(topk_ids.data_ptr(), T * top_k, num_experts, row.data_ptr(), pair.data_ptr(), offsets.data_ptr(),
-                 _stream())
+                 stream)
     return row, pair, offsets
 
 
@@ -830,13 +854,14 @@ def moe_permute(X, row_of_pair, Xs=None):
     """Xs[row_of_pair[t, j]] = X[t] for X [T, H] of any dtype; Xs [rows, H], by default T * top_k rows. Rows that no
     entry names (there are such when pairs were dropped) are not written."""
     torch = _torch()
-    _arg(X, "X", X.dtype, (None, None))
-    T, H = X.shape
-    _arg(row_of_pair, "row_of_pair", torch.int32, (T, None))
-    top_k = row_of_pair.shape[1]
-    Xs = _out_arg(Xs, "Xs", X.dtype, (T * top_k if Xs is None else None, H), X.device)
-    lbq_moe_permute(X.data_ptr(), H * X.element_size(), T, top_k, row_of_pair.data_ptr(), Xs.shape[0], Xs.data_ptr(),
-                    _stream())
+    T, H = _dims(X, "X", 2)
+    top_k = _dims(row_of_pair, "row_of_pair", 2)[1]
+    dev, stream = _here()
+    _arg(X, "X", X.dtype, (T, H), dev)
+    _arg(row_of_pair, "row_of_pair", torch.int32, (T, top_k), dev)
+    rows = T * top_k if Xs is None else _dims(Xs, "Xs", 2)[0]
+    Xs = _out_arg(Xs, "Xs", X.dtype, (rows, H), X, dev)
+    lbq_moe_permute(X.data_ptr(), H * X.element_size(), T, top_k, row_of_pair.data_ptr(), rows, Xs.data_ptr(), stream)
     return Xs
 
 
@@ -845,15 +870,16 @@ def moe_combine(Ys, row_of_pair, weights=None, out=None):
     weights [T, top_k] (None: 1); entries of row_of_pair outside the rows add nothing."""
     torch = _torch()
     dt = _dt(Ys)
-    _arg(Ys, "Ys", Ys.dtype, (None, None))
-    rows, H = Ys.shape
-    _arg(row_of_pair, "row_of_pair", torch.int32, (None, None))
-    T, top_k = row_of_pair.shape
+    rows, H = _dims(Ys, "Ys", 2)
+    T, top_k = _dims(row_of_pair, "row_of_pair", 2)
+    dev, stream = _here()
+    _arg(Ys, "Ys", Ys.dtype, (rows, H), dev)
+    _arg(row_of_pair, "row_of_pair", torch.int32, (T, top_k), dev)
     if weights is not None:
-        _arg(weights, "weights", torch.float32, (T, top_k))
-    out = _out_arg(out, "out", Ys.dtype, (T, H), Ys.device)
+        _arg(weights, "weights", torch.float32, (T, top_k), dev)
+    out = _out_arg(out, "out", Ys.dtype, (T, H), Ys, dev)
     lbq_moe_combine(Ys.data_ptr(), dt, rows, H, row_of_pair.data_ptr(),
-                    weights.data_ptr() if weights is not None else None, T, top_k, out.data_ptr(), _stream())
+                    weights.data_ptr() if weights is not None else None, T, top_k, out.data_ptr(), stream)
     return out
 
 
@@ -862,16 +888,17 @@ def moe_combine_grad(dout, Ys, row_of_pair, weights, dYs=None):
     not written."""
     torch = _torch()
     dt = _dt(Ys)
-    _arg(Ys, "Ys", Ys.dtype, (None, None))
-    rows, H = Ys.shape
-    _arg(row_of_pair, "row_of_pair", torch.int32, (None, None))
-    T, top_k = row_of_pair.shape
-    _arg(dout, "dout", Ys.dtype, (T, H))
-    _arg(weights, "weights", torch.float32, (T, top_k))
-    dYs = _out_arg(dYs, "dYs", Ys.dtype, (rows, H), Ys.device)
-    dweights = torch.empty((T, top_k), dtype=torch.float32, device=Ys.device)
+    rows, H = _dims(Ys, "Ys", 2)
+    T, top_k = _dims(row_of_pair, "row_of_pair", 2)
+    dev, stream = _here()
+    _arg(Ys, "Ys", Ys.dtype, (rows, H), dev)
+    _arg(row_of_pair, "row_of_pair", torch.int32, (T, top_k), dev)
+    _arg(dout, "dout", Ys.dtype, (T, H), dev)
+    _arg(weights, "weights", torch.float32, (T, top_k), dev)
+    dYs = _out_arg(dYs, "dYs", Ys.dtype, (rows, H), Ys, dev)
+    dweights = weights.new_empty((T, top_k))
     lbq_moe_combine_grad(dout.data_ptr(), Ys.data_ptr(), dt, rows, H, row_of_pair.data_ptr(), weights.data_ptr(), T,
-                         top_k, dYs.data_ptr(), dweights.data_ptr(), _stream())
+                         top_k, dYs.data_ptr(), dweights.data_ptr(), stream)
     return dYs, dweights
 
 

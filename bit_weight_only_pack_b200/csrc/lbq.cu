@@ -261,6 +261,31 @@ static lbq_status launch_kernel_ex(const void* fn, dim3 grid, dim3 block, int sm
   return LBQ_OK;
 }
 
+// launch_kernel_ex for clusters of `cluster` blocks.
+static lbq_status launch_cluster(const void* fn, dim3 grid, int cluster, dim3 block, int smem, cudaStream_t st, bool pdl,
+                                 void** args, const char* what) {
+  if (cluster <= 1) return launch_kernel_ex(fn, grid, block, smem, st, pdl, args, what);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e != cudaSuccess)
+    return fail(LBQ_ERR_CUDA, "%s (grid %u, cluster %d, block %u, smem %d, pdl %d): %s", what, grid.x, cluster, block.x,
+                smem, (int)pdl, cudaGetErrorString(e));
+  return LBQ_OK;
+}
+
 static lbq_status run_m1(const uint16_t* X, bool xbf16, const void* image, const Layout& L, void* Y, bool ybf16,
                          void* ws, size_t ws_bytes, cudaStream_t st) {
   const bool asym = L.mode == LBQ_MODE_ASYM;
@@ -1433,73 +1458,119 @@ static uint8_t* noalloc_scratch(cudaStream_t stream, lbq_status* st) {
 // ----------------------------------------------------------------------------
 
 struct W8Plan {
-  int ht, n_tiles, bn, m_tiles, bx, grid;
+  int cg, ht, n_tiles, bn, m_tiles, splits, sub;
 };
 
-// Shape of the tiles: token tiles of bn <= 256 rows, channel tiles of ht <= 128
-// rows. Few tokens: the weights' bytes are the time, and ht is cut so that the
-// tiles fill whole waves of SMs (any height works: the TMA box has ht rows).
-// Many tokens: the MMA time of a tile does not fall with ht, so ht stays 128
-// and bn is cut instead. One cost decides: waves x k-blocks x the longer of the
-// MMA time and the operand loads of a tile, and never below the weights' HBM time.
-static W8Plan plan_w8a8(long long M, int K, int N) {
-  const int sms = num_sms();
-  const int nkb = (K + kW8BK - 1) / kW8BK;
-  W8Plan best{};
-  double best_cost = 0.0;
-  const long long m_min = (M + kW8MaxBn - 1) / kW8MaxBn;
-  for (long long mt = m_min; mt <= m_min + m_min / 2 + 1; ++mt) {
-    const int bn = (int)((((M + mt - 1) / mt) + 15) / 16 * 16);
-    const long long m_tiles = (M + bn - 1) / bn;
-    const long long w0 = ((N + kW8MaxHt - 1) / kW8MaxHt * m_tiles + sms - 1) / sms;
-    for (long long w = w0; w <= w0 + 1; ++w) {
-      const long long nt = std::max<long long>(1, std::min<long long>(N, w * sms / m_tiles));
-      int ht = (int)std::min<long long>(kW8MaxHt, (N + nt - 1) / nt);
-      for (int full = 0; full < 2; ++full) {
-        if (full) ht = std::min(kW8MaxHt, N);
-        const long long tiles = (N + ht - 1) / ht * m_tiles;
-        const double waves = (double)((tiles + sms - 1) / sms);
-        const double mma = std::max(2.0 * bn, 128.0 + bn);    // cycles per k-block: rate, shared-memory reads
-        const double load = (ht + bn) * 128.0 / 48.0;         // cycles per k-block at 48 B per cycle and SM
-        const double cost = waves * (nkb * std::max(mma, load) + 600.0);
-        if (best.bn == 0 || cost < best_cost) {
-          best_cost = cost;
-          best.ht = ht;
-          best.n_tiles = (N + ht - 1) / ht;
-          best.bn = bn;
-          best.m_tiles = (int)m_tiles;
-          best.bx = bn;
-          best.grid = (int)std::min<long long>(tiles, sms);
-        }
+// Blocks of `splits` that fit on the device at once as clusters, one per SM
+// (SMs of one cluster share a GPC, so 4 and 8 leave some idle).
+static int w8_max_clusters(int splits) {
+  static int cached[kW8MaxSplits + 1];
+  static std::once_flag once;
+  std::call_once(once, [] {
+    const void* fn = (const void*)w8a8_gemm_kernel<1>;
+    occupancy_for(fn, kW8Threads, kW8SmemBudget);
+    for (int s = 2; s <= kW8MaxSplits; s *= 2) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)(s * 64));
+      cfg.blockDim = dim3(kW8Threads);
+      cfg.dynamicSmemBytes = kW8SmemBudget;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)s;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&cached[s], fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        cached[s] = 0;
       }
     }
+  });
+  return cached[splits];
+}
+
+// Whole k-blocks per ring stage: as many as leave three stages (issuing a stage
+// costs its warps some 400 clocks whatever its size), at most four.
+static int w8_sub(int ht, int bn, int cg, int K, int extra) {
+  const int block = ((int)align_up((size_t)ht, 8) + bn / cg) * kW8BK;
+  int sub = 4;
+  while (sub > 1 && (3 * sub * block > kW8SmemBudget - extra || sub > std::max(1, K / kW8BK))) --sub;
+  return sub;
+}
+
+// Tiles of the dense product: cg blocks of ht <= 128 channels, token tiles of
+// bn <= 256 rows, splits of K. One estimate in clocks decides: the weights' HBM
+// time, or waves x k-blocks x the longest of the MMAs, their issue and the
+// operand loads of one block, plus what a tile costs once. Few tokens: ht is cut
+// so that the tiles fill the SMs (any multiple of 8 works), or few channels leave
+// SMs over and the blocks of a cluster share a tile's K. Many tokens: pairs of
+// blocks with 256 channels, and bn is cut if that saves a part-filled wave.
+static W8Plan plan_w8a8(long long M, int K, int N) {
+  const int sms = num_sms();
+  const double kb = (K + kW8BK - 1) / kW8BK;
+  const double hbm = (double)K * N / 3400.0;  // clocks at 6.4 TB/s
+  W8Plan best{};
+  double best_cost = 0.0;
+  auto consider = [&](int cg, int ht, int bn, int splits) {
+    const long long m_tiles = (M + bn - 1) / bn, n_tiles = (N + cg * ht - 1) / (cg * ht);
+    if (m_tiles * n_tiles > 0x3FFFFFFF) return;
+    const int sub = w8_sub(ht, bn, cg, K, 1024 + kW8MaxHt * kW8BK);
+    double waves = (double)((m_tiles * n_tiles * cg + sms - 1) / sms);
+    double once = 2500.0 + 12.0 * bn;
+    if (splits > 1) {
+      if (waves > 1.0 || m_tiles * n_tiles > w8_max_clusters(splits) || K / kW8BK < splits * sub) return;
+      once += 3500.0;
+    }
+    const double mma = 4.0 * std::max(0.5 * bn, 45.0) + 150.0 / sub, issue = 450.0 / sub;
+    const double load = (ht + (double)bn / cg) * kW8BK / 56.0;
+    const double cost = std::max(hbm, waves * std::ceil(kb / splits) * std::max(std::max(mma, issue), load)) + once;
+    if (best.bn == 0 || cost < best_cost) {
+      best_cost = cost;
+      best = W8Plan{cg, ht, (int)n_tiles, bn, (int)m_tiles, splits, sub};
+    }
+  };
+  const long long m_min = (M + kW8MaxBn - 1) / kW8MaxBn;
+  for (long long mt = m_min; mt <= m_min + m_min / 4 + 1; ++mt) {
+    const int bn1 = (int)align_up((size_t)((M + mt - 1) / mt), 16), bn2 = (int)align_up((size_t)((M + mt - 1) / mt), 32);
+    const int full = std::min(kW8MaxHt, (int)align_up((size_t)N, 8));
+    if (N > kW8MaxHt && M > 64) consider(2, kW8MaxHt, bn2, 1);
+    consider(1, full, bn1, 1);
+    const long long m_tiles = (M + bn1 - 1) / bn1;
+    const long long w0 = ((long long)((N + kW8MaxHt - 1) / kW8MaxHt) * m_tiles + sms - 1) / sms;
+    if (w0 * sms >= m_tiles) {  // ht that fills w0 waves
+      const long long nt = w0 * sms / m_tiles;
+      consider(1, (int)std::min<long long>(full, align_up((size_t)((N + nt - 1) / nt), 8)), bn1, 1);
+    }
+    if (bn1 <= kW8MaxSplitBn && m_tiles == 1)
+      for (int s = 2; s <= kW8MaxSplits; s *= 2) {
+        const int nt = w8_max_clusters(s);
+        if (nt > 0)
+          consider(1, (int)std::min<long long>(full, align_up((size_t)((N + nt - 1) / nt), 8)), bn1, s);
+      }
   }
   return best;
 }
 
 // Routed: the rows of each expert are known on the device only, so the tile is
-// chosen for the mean run of an expert.
-static W8Plan plan_moe_w8a8(int M, int N, int E) {
+// chosen for the mean run of an expert; the MMAs and copies of a shorter run are
+// cut to its rows.
+static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   W8Plan p{};
   const int mean = (M + E - 1) / E;
-  p.bn = mean <= 8 ? 16 : mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 90 ? 128 : 256;
-  p.bx = std::min(p.bn, 32);
-  p.ht = std::min(kW8MaxHt, N);
-  p.n_tiles = (N + p.ht - 1) / p.ht;
-  p.m_tiles = 0;
-  p.grid = (int)std::min<long long>((long long)p.n_tiles * ((long long)M / p.bn + std::min(E, M)), num_sms());
+  p.cg = mean > 48 && N > kW8MaxHt ? 2 : 1;
+  p.bn = mean <= 4 ? 16 : mean <= 12 ? 32 : mean <= 24 ? 64 : mean <= 48 ? 128 : 256;
+  const int span = p.cg * kW8MaxHt;
+  p.n_tiles = (N + span - 1) / span;
+  p.ht = std::min(kW8MaxHt, (int)align_up((size_t)((N + p.cg * p.n_tiles - 1) / (p.cg * p.n_tiles)), 8));
+  p.n_tiles = (N + p.cg * p.ht - 1) / (p.cg * p.ht);
+  p.splits = 1;
+  p.sub = w8_sub(p.ht, p.bn, p.cg, K, 1024 + kW8MaxHt * kW8BK + (E + 1) * (int)sizeof(int));
   return p;
 }
 
 static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int N, int E, const int32_t* offsets,
                            const int8_t* wq, const float* sw, void* Y, bool ybf16, bool pdl, cudaStream_t st) {
-  const W8Plan p = offsets ? plan_moe_w8a8(M, N, E) : plan_w8a8(M, K, N);
-  CUtensorMap tw, tx;
-  if (!make_tmap_2d(&tw, wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K, (uint64_t)E * (uint64_t)N, (uint64_t)K,
-                    kW8BK, (uint32_t)p.ht, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)K, (uint64_t)M, (uint64_t)K, kW8BK,
-                    (uint32_t)p.bx, CU_TENSOR_MAP_SWIZZLE_128B))
-    return fail(LBQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the W8A8 operands");
+  const W8Plan p = offsets ? plan_moe_w8a8(M, K, N, E) : plan_w8a8(M, K, N);
   W8a8Args a{};
   a.Y = Y;
   a.sx = sx;
@@ -1507,22 +1578,52 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
   a.offsets = offsets;
   a.M = M; a.N = N; a.E = E;
   a.ht = p.ht; a.n_tiles = p.n_tiles;
-  a.bn = p.bn; a.m_tiles = p.m_tiles; a.bx = p.bx;
-  a.k_blocks = (K + kW8BK - 1) / kW8BK;
-  a.a_bytes = (int)align_up((size_t)p.ht, 8) * kW8BK;
-  a.stage_bytes = a.a_bytes + p.bn * kW8BK;
+  a.bn = p.bn; a.m_tiles = p.m_tiles;
+  a.sub = p.sub; a.splits = p.splits;
+  a.k_whole = K / kW8BK;
+  a.k_tail = K % kW8BK != 0;
+  a.k_stages = (a.k_whole + p.sub - 1) / p.sub + a.k_tail;
+  a.a_sub = (int)align_up((size_t)p.ht, 8) * kW8BK;
+  a.b_off = p.sub * a.a_sub;
+  a.stage_bytes = a.b_off + p.sub * (p.bn / p.cg) * kW8BK;
   a.acc_stride = (int)align_up((size_t)p.bn, 32);
   a.tmem_cols = 64;
   while (a.tmem_cols < 2 * a.acc_stride) a.tmem_cols *= 2;
   a.y_bf16 = ybf16 ? 1 : 0;
+
+  W8Maps maps;
+  const uint64_t w_rows = (uint64_t)E * (uint64_t)N, k64 = (uint64_t)K;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
+  bool ok = true;
+  auto encode = [&](CUtensorMap* whole, CUtensorMap* tail, const void* base, uint64_t rows, int box) {
+    if (a.k_whole)
+      ok = ok && make_tmap_3d(whole, base, u8, kW8BK, rows, (uint64_t)a.k_whole, k64, kW8BK, kW8BK, (uint32_t)box,
+                              (uint32_t)p.sub, swz);
+    if (a.k_tail) ok = ok && make_tmap_2d(tail, base, u8, 1, k64, rows, k64, kW8BK, (uint32_t)box, swz);
+  };
+  encode(&maps.w, &maps.w_tail, wq, w_rows, p.ht);
+  if (!offsets) {
+    encode(&maps.x[0], &maps.x_tail[0], xq, (uint64_t)M, p.bn / p.cg);
+  } else {
+    for (int i = 0; i < kW8XMaps && (16 << i) <= p.bn / p.cg; ++i)
+      encode(&maps.x[i], &maps.x_tail[i], xq, (uint64_t)M, 16 << i);
+  }
+  if (!ok) return fail(LBQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the W8A8 operands");
+
   // alignment, the slack behind the ring, and the routed form's tile counts
   const int extra = 1024 + kW8MaxHt * kW8BK + (offsets ? (E + 1) * (int)sizeof(int) : 0);
   a.stages = std::min(kW8MaxStages, (kW8SmemBudget - extra) / a.stage_bytes);
   const int smem = a.stages * a.stage_bytes + extra;
-  const void* fn = (const void*)w8a8_gemm_kernel;
+  const void* fn = p.cg == 2 ? (const void*)w8a8_gemm_kernel<2> : (const void*)w8a8_gemm_kernel<1>;
   occupancy_for(fn, kW8Threads, smem);
-  void* args[] = {&tw, &tx, &a};
-  return launch_kernel_ex(fn, dim3(p.grid), dim3(kW8Threads), smem, st, pdl, args, "W8A8 GEMM launch");
+  // routed: at most one part-filled token tile per expert that has rows
+  const long long m_tiles = offsets ? (long long)M / p.bn + std::min(E, M) : p.m_tiles;
+  const int share = p.cg * p.splits;  // blocks per tile: a cluster
+  const long long units = p.splits > 1 ? m_tiles * p.n_tiles : std::min<long long>(m_tiles * p.n_tiles, num_sms() / p.cg);
+  void* args[] = {&maps, &a};
+  return launch_cluster(fn, dim3((unsigned)(units * share)), share, dim3(kW8Threads), smem, st, pdl, args,
+                        "W8A8 GEMM launch");
 }
 
 static lbq_status run_quantize_rows(const void* X, int x_dtype, int M, int K, int8_t* xq, float* sx, cudaStream_t st) {

@@ -140,14 +140,16 @@ __global__ void __launch_bounds__(256) quantize_int8_weight_kernel(const float* 
 
 // ---------------------------------------------------------------------------- product
 
-constexpr int kW8BK = 128;        // k per ring stage: one 128-byte swizzle span, four MMAs of K = 32
-constexpr int kW8MaxHt = 128;     // channels per tile (MMA M, TMEM lanes)
+constexpr int kW8BK = 128;        // k per block: one 128-byte swizzle span, four MMAs of K = 32
+constexpr int kW8MaxHt = 128;     // channels per block and tile (TMEM lanes)
 constexpr int kW8MaxBn = 256;     // tokens per tile (MMA N)
 constexpr int kW8MaxStages = 16;
 constexpr int kW8Threads = 192;   // TMA producer, MMA issuer, four epilogue warps
+constexpr int kW8MaxSplits = 8;   // blocks that share one tile's K (one cluster)
+constexpr int kW8MaxSplitBn = 64; // ... of at most this many tokens
 constexpr int kW8MaxExperts = 2048;
 constexpr int kW8MaxK = 65536;        // 2^16 products of at most 2^14: the sum stays in int32
-constexpr int kW8SmemBudget = 226 * 1024;  // dynamic; the static barriers take the rest of 227 KB
+constexpr int kW8SmemBudget = 222 * 1024;  // dynamic; barriers and the epilogue's scales take the rest of 227 KB
 
 struct W8a8Args {
   void* Y;                  // [M][N]
@@ -155,29 +157,143 @@ struct W8a8Args {
   const float* sw;          // [E][N]
   const int32_t* offsets;   // [E + 1] first row of each expert's run, or null (dense)
   int M, N, E;
-  int ht, n_tiles;          // channels per tile, tiles along N
+  int ht, n_tiles;          // channels per block, tiles along N (CG ht channels each)
   int bn, m_tiles;          // tokens per tile; tiles along M (dense)
-  int bx;                   // token rows per TMA box (bn is a multiple)
-  int k_blocks, stages, a_bytes, stage_bytes;
+  int k_stages, splits;     // ring stages of a tile's K; blocks that share them (CG = 1)
+  int sub;                  // whole 128-k blocks per ring stage
+  int k_whole, k_tail;      // K / 128; 1 if K % 128: one more stage, of the rest
+  int stages, a_sub, b_off, stage_bytes;  // bytes: a weight block, offset of the token blocks, a stage
   int acc_stride, tmem_cols;
   int y_bf16;
 };
 
+constexpr int kW8XMaps = 5;
+
+// Tensor maps. Whole blocks: dimensions (128 bytes of k, row, k-block), so one
+// copy fetches `sub` blocks, each a 128-byte swizzled tile (one copy per operand
+// and stage: issuing a copy costs its warp some 150 clocks). Rest of K:
+// dimensions (k, row), zeros past K. x[i] has boxes of x_rows(i) token rows:
+// dense, only the tile's (i = 0); routed, 16 << i, so that a short run of rows
+// is not fetched as a full tile.
+struct W8Maps {
+  CUtensorMap w, x[kW8XMaps], w_tail, x_tail[kW8XMaps];
+};
+
 // Instruction descriptor of kind::i8: D = S32 (2), A = B = S8 (1), both
-// K-major, M = 128, N = n.
-__host__ __device__ constexpr uint32_t umma_idesc_i8(int n) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+// K-major, M = m, N = n.
+__host__ __device__ constexpr uint32_t umma_idesc_i8(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+template <int CG>
 __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "setp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-               :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+  if constexpr (CG == 1)
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
 }
 
-// One output tile: channels n0 .. n0 + nh - 1 (of expert e), rows m0 .. m0 + mh - 1.
+// Arrive on `bar` (in both blocks of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void w8_commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    umma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void w8_tmem_alloc(uint32_t* dst, uint32_t cols) {
+  if constexpr (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void w8_tmem_dealloc(uint32_t tmem, uint32_t cols) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster; writes before it are visible after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this block's shared-memory location `addr` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+// mbar_wait_sleep that also orders what other blocks of the cluster did before their arrivals.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kSleepPolls; ++i) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepHintNs) : "memory");
+    if (ok) return true;
+  }
+  atomicOr(&g_device_error, kDevErrTimeout);
+  return false;
+}
+
+// Tiled TMA loads into this block's shared memory; bytes counted on the barrier
+// at shared::cluster address `bar` (for a pair: the first block's).
+template <int CG>
+__device__ __forceinline__ void w8_load_blocks(uint32_t dst, const CUtensorMap* m, int row, int kb, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(kb), "r"(bar) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(kb), "r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void w8_load_tail(uint32_t dst, const CUtensorMap* m, int row, int k, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(k), "r"(row), "r"(bar) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                 "[%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(k), "r"(row), "r"(bar) : "memory");
+}
+
+// One output tile: channels n0 .. n0 + nh - 1 (this block's; of expert e), rows m0 .. m0 + mh - 1.
 struct W8Tile {
   int n0, nh, m0, mh, e;
 };
@@ -185,7 +301,8 @@ struct W8Tile {
 // Tile `t` of the call. Dense: bands of token tiles (stream_k.cuh). Routed:
 // start[e] = token tiles of the experts before e (shared memory), channels
 // inner, so an expert's tiles are neighbours.
-__device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, int t) {
+template <int CG>
+__device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, int t, int rank) {
   W8Tile w;
   int nt, mt;
   if (a.offsets == nullptr) {
@@ -207,9 +324,25 @@ __device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, i
     w.m0 = first + (mt - start[lo]) * a.bn;
     w.mh = min(a.bn, end - w.m0);
   }
-  w.n0 = nt * a.ht;
-  w.nh = min(a.ht, a.N - w.n0);
+  w.n0 = (CG * nt + (CG == 2 ? rank : 0)) * a.ht;
+  w.nh = max(0, min(a.ht, a.N - w.n0));
   return w;
+}
+
+// MMA N of a tile of mh rows: 16 columns a step, 32 for a pair.
+template <int CG>
+__device__ __forceinline__ int w8_mma_n(int mh) { return (mh + 16 * CG - 1) / (16 * CG) * (16 * CG); }
+
+// The map of a tile's token rows (its index) and that map's rows per box.
+template <int CG>
+__device__ __forceinline__ int w8_x_map(const W8a8Args& a, int mh) {
+  if (a.offsets == nullptr) return 0;
+  const int rows = w8_mma_n<CG>(mh) / CG;  // a multiple of 16
+  return rows <= 16 ? 0 : 32 - __clz((rows - 1) >> 4);
+}
+template <int CG>
+__device__ __forceinline__ int w8_x_rows(const W8a8Args& a, int map) {
+  return a.offsets == nullptr ? a.bn / CG : 16 << map;
 }
 
 // start[0 .. E] of the routed form, by the whole block (contiguous ranges of
@@ -242,26 +375,93 @@ __device__ __forceinline__ void w8_expert_tiles(const W8a8Args& a, int* start) {
   __syncthreads();
 }
 
-// Warp 0: TMA producer (per k-block the tile's weight rows and token rows, both
-// 128-byte swizzled); warp 1: TMEM owner and MMA issuer; warps 2..5: epilogue,
-// one TMEM lane quarter each (lane = channel), into Y with 64-byte row segments
-// per warp. Two accumulators alternate, so the MMAs of a tile run while the last
-// one is written. Persistent: one block per SM takes every gridDim.x-th tile and
-// the ring runs on across tiles.
+template <bool BF16>
+__device__ __forceinline__ uint16_t w8_round(float f) {
+  return BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool w8_elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// Position in the ring, without a division per step.
+struct W8Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Columns j .. j + n - 1 (n <= 32) of the block's accumulator into Y: lane =
+// channel, so the warp writes 64 contiguous bytes of every token's row.
+template <bool BF16>
+__device__ __forceinline__ void w8_store32(const uint32_t (&v)[32], float sw, const float* sxs, uint16_t* y, int N, int n,
+                                           bool row_ok) {
+  uint16_t h[32];
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 s4 = *reinterpret_cast<const float4*>(sxs + i);
+    h[i] = w8_round<BF16>(((float)(int)v[i] * sw) * s4.x);
+    h[i + 1] = w8_round<BF16>(((float)(int)v[i + 1] * sw) * s4.y);
+    h[i + 2] = w8_round<BF16>(((float)(int)v[i + 2] * sw) * s4.z);
+    h[i + 3] = w8_round<BF16>(((float)(int)v[i + 3] * sw) * s4.w);
+  }
+  if (!row_ok) return;
+  if (n >= 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) y[(size_t)i * N] = h[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) y[(size_t)i * N] = h[i];
+  }
+}
+
+// Warp 0: TMA producer (per ring stage one copy of the tile's weight rows and one
+// of its token rows, `sub` blocks of 128 k each, 128-byte swizzled);
+// warp 1: TMEM owner and MMA issuer; warps 2..5: epilogue, one TMEM lane quarter
+// each (lane = channel). Two accumulators alternate, so the MMAs of a tile run
+// while the last one is written. Persistent: every block (CG = 1) or pair of
+// blocks (CG = 2) takes every so-manieth tile and the ring runs on across tiles.
 //
-// A tile of fewer than 128 channels loads only its own rows; the MMA's other
-// rows read whatever follows in shared memory (integers, so no NaN can arise)
-// and their lanes are not stored. The ring ends with that much slack.
+// Warps 0 and 1 run their loops converged and elect a lane for each issue: with
+// warp-uniform control flow the descriptors stay in uniform registers. A loop of
+// wait, four MMAs and commit measured 340 clocks so (128 x 16 tile; 512, the full
+// rate, at 128 x 256) against 690 with one lane branching off for the whole loop.
+//
+// CG = 1: a tile of fewer than 128 channels loads only its own rows; the MMA's
+// other rows read whatever follows in shared memory (integers, so no NaN can
+// arise) and their lanes are not stored. The ring ends with that much slack.
+// With splits > 1 the blocks of a cluster share the K of one tile: each leaves
+// its int32 sums in its own shared memory, and every block adds all of them for
+// its share of the tokens (integers: in any order the same).
+//
+// CG = 2: two blocks of a cluster share one MMA of 256 channels: each loads its
+// own 128 weight rows and half of the token rows, so the token operand crosses
+// shared memory once per pair. The first block issues the MMAs; copies of both
+// are counted on its barrier, and its commits arrive in both blocks.
+template <int CG>
 __global__ void __launch_bounds__(kW8Threads, 1)
-    w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
-                     const W8a8Args a) {
+    w8a8_gemm_kernel(const __grid_constant__ W8Maps maps, const W8a8Args a) {
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kW8MaxStages], empty_bar[kW8MaxStages], d_full[2], d_empty[2];
+  __shared__ __align__(16) float sx_sh[4][kW8MaxBn];  // each epilogue warp's copy of its tile's token scales
   __shared__ uint32_t tmem_base_sh;
+  __shared__ int split_ok;
   uint8_t* ring = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
   int* start = reinterpret_cast<int*>(ring + (size_t)a.stages * a.stage_bytes + kW8MaxHt * kW8BK);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool split = CG == 1 && a.splits > 1;
+  const int rank = (CG == 2 || split) ? (int)cluster_rank() : 0;
+  const int share = CG == 2 ? 2 : a.splits;  // blocks per tile
   w8_griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -270,18 +470,15 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);
+      mbar_init(&d_empty[i], 4 * CG);
     }
     fence_barrier_init();
+    split_ok = 0;
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 :: "r"(smem_u32(&tmem_base_sh)), "r"((uint32_t)a.tmem_cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tw);
-    tma_prefetch_desc(&tx);
+  if (warp == 1) w8_tmem_alloc<CG>(&tmem_base_sh, (uint32_t)a.tmem_cols);
+  if (warp == 0 && w8_elect()) {
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.x[0]);
   }
   if (a.offsets != nullptr) {
     w8_griddep_wait();  // the offsets come from a kernel before
@@ -289,110 +486,190 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the other block's barriers are ready
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const int total = (a.offsets == nullptr ? a.m_tiles : start[a.E]) * a.n_tiles;
+  const int unit = blockIdx.x / share, units = gridDim.x / share;
+  // this block's stages of each of its tiles
+  const int ks0 = split ? a.k_stages * rank / a.splits : 0;
+  const int ks1 = split ? a.k_stages * (rank + 1) / a.splits : a.k_stages;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // the weights of the first stages are requested before the kernel that
-      // writes the activations has ended
-      int pre = 0;
-      for (int tile = blockIdx.x; tile < total && pre < a.stages; tile += gridDim.x) {
-        const W8Tile w = w8_tile(a, start, tile);
-        const int boxes = (w.mh + a.bx - 1) / a.bx;
-        for (int kb = 0; kb < a.k_blocks && pre < a.stages; ++kb, ++pre) {
-          mbar_arrive_expect_tx(&full_bar[pre], (uint32_t)((a.ht + boxes * a.bx) * kW8BK));
-          tma_load_2d(ring + (size_t)pre * a.stage_bytes, &tw, kb * kW8BK, w.e * a.N + w.n0, &full_bar[pre]);
-        }
+    const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(full_bar);
+    const uint32_t full_c = CG == 2 ? cluster_addr(full_u, 0) : full_u;  // the barriers that count the bytes
+    // weights of k-stage ks of tile w into ring stage `slot`, and the announcement of all the stage's bytes
+    const int tail_stage = a.k_tail ? a.k_stages - 1 : -1;
+    auto load_w = [&](const W8Tile& w, int xrows, int ks, int slot) {
+      const uint32_t st = ring_u + (uint32_t)(slot * a.stage_bytes), bar = full_c + 8u * slot;
+      const bool tail = ks == tail_stage;
+      if (w8_elect()) {
+        if (CG == 1 || rank == 0)
+          mbar_arrive_expect_tx(&full_bar[slot], (uint32_t)(CG * (tail ? 1 : a.sub) * (a.ht + xrows) * kW8BK));
+        if (!tail) w8_load_blocks<CG>(st, &maps.w, w.e * a.N + w.n0, ks * a.sub, bar);
+        else w8_load_tail<CG>(st, &maps.w_tail, w.e * a.N + w.n0, a.k_whole * kW8BK, bar);
       }
-      w8_griddep_wait();
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const W8Tile w = w8_tile(a, start, tile);
-        const int boxes = (w.mh + a.bx - 1) / a.bx;
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
-          const int s = it % a.stages;
-          uint8_t* st = ring + (size_t)s * a.stage_bytes;
-          if (it >= pre) {
-            if (!mbar_wait_sleep(&empty_bar[s], ((it / a.stages) & 1) ^ 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&full_bar[s], (uint32_t)((a.ht + boxes * a.bx) * kW8BK));
-            tma_load_2d(st, &tw, kb * kW8BK, w.e * a.N + w.n0, &full_bar[s]);
-          }
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(st + a.a_bytes + b * a.bx * kW8BK, &tx, kb * kW8BK, w.m0 + b * a.bx, &full_bar[s]);
-        }
+    };
+    auto load_x = [&](int map, int row, int ks, int slot) {
+      const uint32_t st = ring_u + (uint32_t)(slot * a.stage_bytes + a.b_off), bar = full_c + 8u * slot;
+      if (w8_elect()) {
+        if (ks != tail_stage) w8_load_blocks<CG>(st, &maps.x[map], row, ks * a.sub, bar);
+        else w8_load_tail<CG>(st, &maps.x_tail[map], row, a.k_whole * kW8BK, bar);
       }
-      // every copy this block issued lands before it may exit
-      for (int v = max(0, it - a.stages); v < it; ++v)
-        if (!mbar_wait_sleep(&full_bar[v % a.stages], (v / a.stages) & 1)) break;
+    };
+    // the weights of the first stages are requested before the kernel that
+    // writes the activations has ended
+    int pre = 0;
+    for (int tile = unit; tile < total && pre < a.stages; tile += units) {
+      const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+      const int xrows = w8_x_rows<CG>(a, w8_x_map<CG>(a, w.mh));
+      for (int ks = ks0; ks < ks1 && pre < a.stages; ++ks, ++pre) load_w(w, xrows, ks, pre);
+    }
+    w8_griddep_wait();
+    W8Ring r;
+    int it = 0;
+    bool ok = true;
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+      const int map = w8_x_map<CG>(a, w.mh), xrows = w8_x_rows<CG>(a, map);
+      const int x0 = w.m0 + (CG == 2 ? rank * (w8_mma_n<2>(w.mh) / 2) : 0);  // a pair: half of the MMA's N each
+      for (int ks = ks0; ks < ks1; ++ks, ++it) {
+        if (it >= pre) {
+          ok = mbar_wait_sleep(&empty_bar[r.s], r.phase ^ 1);
+          if (!ok) break;
+          load_w(w, xrows, ks, r.s);
+        }
+        load_x(map, x0, ks, r.s);
+        r.next(a.stages);
+      }
+    }
+    // before the block may exit, its last copies have landed and the commits
+    // on its barriers have arrived (after a timed-out wait: the copies, which
+    // had that wait's time as well)
+    for (int v = max(0, it - a.stages); v < it; ++v) {
+      const int s = v % a.stages;
+      if (!mbar_wait_sleep(&empty_bar[s], (v / a.stages) & 1)) {
+        if (CG == 1) mbar_wait_sleep(&full_bar[s], (v / a.stages) & 1);
+        break;
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int it = 0, t_iter = 0;
+    if (CG == 1 || rank == 0) {
+      W8Ring r;
+      const uint32_t ring_u = smem_u32(ring);
+      int t_iter = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++t_iter) {
-        const W8Tile w = w8_tile(a, start, tile);
-        const uint32_t idesc = umma_idesc_i8((w.mh + 15) & ~15);
+      for (int tile = unit; tile < total && ok; tile += units, ++t_iter) {
+        const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+        const uint32_t idesc = umma_idesc_i8(128 * CG, w8_mma_n<CG>(w.mh));
         const int ai = t_iter & 1;
         const uint32_t d = tmem + (uint32_t)(ai * a.acc_stride);
-        if (t_iter >= 2 && !mbar_wait_sleep(&d_empty[ai], ((t_iter >> 1) & 1) ^ 1)) break;
-        tc_fence_after();
-        for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
-          const int s = it % a.stages;
-          if (!mbar_wait_sleep(&full_bar[s], (it / a.stages) & 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t st = smem_u32(ring + (size_t)s * a.stage_bytes);
-          const uint64_t da = umma_desc_sw128(st), db = umma_desc_sw128(st + (uint32_t)a.a_bytes);
-#pragma unroll
-          for (uint32_t kk = 0; kk < 4; ++kk)
-            umma_i8(d, da + kk * 2, db + kk * 2, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&empty_bar[s]);
+        if (t_iter >= 2) {
+          ok = mbar_wait_cluster(&d_empty[ai], ((t_iter >> 1) & 1) ^ 1);
+          if (!ok) break;
         }
-        if (ok) umma_commit(&d_full[ai]);
+        tc_fence_after();
+        // 16-byte units between a stage's blocks
+        const uint64_t a_step = (uint64_t)((uint32_t)a.a_sub >> 4);
+        const uint64_t b_step = (uint64_t)((uint32_t)(w8_x_rows<CG>(a, w8_x_map<CG>(a, w.mh)) * kW8BK) >> 4);
+        for (int ks = ks0; ks < ks1; ++ks) {
+          ok = mbar_wait_sleep(&full_bar[r.s], r.phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = ring_u + (uint32_t)(r.s * a.stage_bytes);
+          // blocks of this stage (past K they are zeros: not multiplied)
+          const int nb = a.k_tail && ks == a.k_stages - 1 ? 1 : min(a.sub, a.k_whole - ks * a.sub);
+          if (w8_elect()) {
+            uint64_t da = umma_desc_sw128(st), db = umma_desc_sw128(st + (uint32_t)a.b_off);
+            for (int u = 0; u < nb; ++u) {
+#pragma unroll
+              for (uint32_t kk = 0; kk < 4; ++kk)
+                umma_i8<CG>(d, da + kk * 2, db + kk * 2, idesc, (ks > ks0 || u > 0 || kk > 0) ? 1u : 0u);
+              da += a_step;
+              db += b_step;
+            }
+            w8_commit<CG>(&empty_bar[r.s]);
+          }
+          r.next(a.stages);
+        }
+        if (ok && w8_elect()) w8_commit<CG>(&d_full[ai]);
       }
     }
   } else {
     w8_griddep_wait();  // sx is read (and Y written) after the kernels before
     const int q = warp & 3;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t d_empty_c = CG == 2 ? cluster_addr(smem_u32(d_empty), 0) : smem_u32(d_empty);
+    float* sxs = sx_sh[warp - 2];
     int t_iter = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++t_iter) {
-      const W8Tile w = w8_tile(a, start, tile);
+    for (int tile = unit; tile < total; tile += units, ++t_iter) {
+      const W8Tile w = w8_tile<CG>(a, start, tile, rank);
       const int ai = t_iter & 1;
-      const int r = 32 * q + lane;  // channel within the tile
+      const int r = 32 * q + lane;  // channel within the block's part of the tile
       const bool row_ok = r < w.nh;
       const float sw = row_ok ? __ldg(a.sw + (size_t)w.e * a.N + w.n0 + r) : 0.0f;
+      __syncwarp();  // the last tile's scales have been read
+      for (int j = lane; j < w.mh; j += 32) sxs[j] = __ldg(a.sx + w.m0 + j);
+      __syncwarp();
       if (!mbar_wait_sleep(&d_full[ai], (t_iter >> 1) & 1)) break;
       tc_fence_after();
+      if (split) {  // the sums, [token][channel], over the ring: every copy and MMA of this block is done
+        int* part = reinterpret_cast<int*>(ring);
+        for (int j = 0; j < w.mh; j += 32) {
+          uint32_t v[32];
+          tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + j), v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (j + i < w.mh) part[(j + i) * kW8MaxHt + r] = (int)v[i];
+        }
+        if (tid == 64) split_ok = 1;
+        continue;
+      }
       for (int j = 0; j < w.mh; j += 32) {
-        const float sxl = j + lane < w.mh ? __ldg(a.sx + w.m0 + j + lane) : 0.0f;
         uint32_t v[32];
         tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + j), v);
         if (j + 32 >= w.mh) {  // the accumulator is in registers: the MMAs may fill it again
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&d_empty[ai]);
+          if (lane == 0) mbar_arrive_cluster(d_empty_c + 8u * ai);
         }
         uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + j) * a.N + w.n0 + r;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float f = ((float)(int)v[i] * sw) * __shfl_sync(0xFFFFFFFFu, sxl, i);
-          const uint16_t h =
-              a.y_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
-          if (row_ok && j + i < w.mh) y[(size_t)i * a.N] = h;
-        }
+        if (a.y_bf16) w8_store32<true>(v, sw, sxs + j, y, a.N, w.mh - j, row_ok);
+        else w8_store32<false>(v, sw, sxs + j, y, a.N, w.mh - j, row_ok);
       }
     }
   }
+  __syncwarp();
 
+  if (split) {
+    cluster_sync();  // every block's sums are in place
+    if (warp >= 2 && unit < total) {
+      const W8Tile w = w8_tile<CG>(a, start, unit, rank);
+      const int r = tid - 64;
+      bool ok = true;
+      for (int c = 0; c < a.splits; ++c) ok = ok && ld_cluster(cluster_addr(smem_u32(&split_ok), (uint32_t)c)) != 0;
+      if (ok && r < w.nh) {
+        const float sw = __ldg(a.sw + (size_t)w.e * a.N + w.n0 + r);
+        const uint32_t part = smem_u32(ring) + 4u * (uint32_t)r;
+        for (int t = rank; t < w.mh; t += a.splits) {
+          int sum = 0;
+#pragma unroll
+          for (int c = 0; c < kW8MaxSplits; ++c)
+            if (c < a.splits) sum += ld_cluster(cluster_addr(part + (uint32_t)(t * kW8MaxHt * 4), (uint32_t)c));
+          const float f = ((float)sum * sw) * __ldg(a.sx + w.m0 + t);
+          static_cast<uint16_t*>(a.Y)[(size_t)(w.m0 + t) * a.N + w.n0 + r] =
+              a.y_bf16 ? w8_round<true>(f) : w8_round<false>(f);
+        }
+      }
+      __syncwarp();
+    }
+  }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2 || split) cluster_sync();  // no block's shared memory or barriers are needed any more
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
-                 :: "r"(tmem), "r"((uint32_t)a.tmem_cols) : "memory");
+    w8_tmem_dealloc<CG>(tmem, (uint32_t)a.tmem_cols);
   }
 }
 

@@ -1568,8 +1568,55 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   return p;
 }
 
+static int g_w8_fuse_max = 2;
+static int g_w8_gemv_max = kW8GvMaxM;  // test hook: largest M on the CUDA-core product
+
+template <bool QUANT, bool BF16>
+static const void* w8_gemv_kernel(int M) {
+  if (M == 1) return (const void*)w8a8_gemv_kernel<1, QUANT, BF16>;
+  if (M == 2) return (const void*)w8a8_gemv_kernel<2, QUANT, BF16>;
+  if (M <= 4) return (const void*)w8a8_gemv_kernel<4, QUANT, BF16>;
+  return (const void*)w8a8_gemv_kernel<8, QUANT, BF16>;
+}
+
+// Whether M tokens of K codes go to the CUDA-core product: the codes of the
+// padded batch have to fit beside a second block on the SM.
+static bool w8_gemv_ok(int M, int K, int N) {
+  const int mb = M <= 2 ? M : M <= 4 ? 4 : 8;
+  if (M > g_w8_gemv_max || (long long)mb * K > 100 * 1024) return false;
+  return M <= 4 || (long long)K * N <= (1LL << 25);
+}
+// ... and whether it quantises them itself (they are kept in registers meanwhile).
+static bool w8_gemv_fused(int M, int K, int N) {
+  return M <= g_w8_fuse_max && w8_gemv_ok(M, K, N) && (long long)M * K <= kW8GvFusedVpt * 8 * kW8GvWarps * 32;
+}
+
+// x_dtype < 0: X holds codes with the scales sx.
+static lbq_status run_w8a8_gemv(const void* X, int x_dtype, const float* sx, int M, int K, int N, const int8_t* wq,
+                                const float* sw, void* Y, bool ybf16, bool pdl, cudaStream_t st) {
+  W8GemvArgs a{};
+  a.X = X;
+  a.sx = sx;
+  a.wq = wq;
+  a.sw = sw;
+  a.Y = Y;
+  a.M = M; a.K = K; a.N = N;
+  a.pairs = (N + kW8GvRows - 1) / kW8GvRows;
+  a.y_bf16 = ybf16 ? 1 : 0;
+  const void* fn = x_dtype < 0                    ? w8_gemv_kernel<false, false>(M)
+                   : x_dtype == LBQ_DTYPE_BF16 ? w8_gemv_kernel<true, true>(M)
+                                               : w8_gemv_kernel<true, false>(M);
+  const int mb = M <= 2 ? M : M <= 4 ? 4 : 8;
+  const int smem = mb * K;
+  const int occ = std::min(2, occupancy_for(fn, kW8GvWarps * 32, smem));
+  const int grid = std::min((a.pairs + kW8GvWarps - 1) / kW8GvWarps, num_sms() * occ);
+  void* args[] = {&a};
+  return launch_kernel_ex(fn, dim3(grid), dim3(kW8GvWarps * 32), smem, st, pdl, args, "W8A8 GEMV launch");
+}
+
 static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int N, int E, const int32_t* offsets,
                            const int8_t* wq, const float* sw, void* Y, bool ybf16, bool pdl, cudaStream_t st) {
+  if (!offsets && w8_gemv_ok(M, K, N)) return run_w8a8_gemv(xq, -1, sx, M, K, N, wq, sw, Y, ybf16, pdl, st);
   const W8Plan p = offsets ? plan_moe_w8a8(M, K, N, E) : plan_w8a8(M, K, N);
   W8a8Args a{};
   a.Y = Y;
@@ -1626,16 +1673,34 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
                         "W8A8 GEMM launch");
 }
 
+template <bool BF16>
+static const void* quantize_rows_kernel(int vpt, bool warp) {
+  if (warp)
+    return vpt <= 2   ? (const void*)quantize_int8_rows_warp_kernel<BF16, 2>
+           : vpt <= 4 ? (const void*)quantize_int8_rows_warp_kernel<BF16, 4>
+                      : (const void*)quantize_int8_rows_warp_kernel<BF16, 8>;
+  return vpt == 1   ? (const void*)quantize_int8_rows_kernel<BF16, 1>
+         : vpt == 2 ? (const void*)quantize_int8_rows_kernel<BF16, 2>
+         : vpt == 4 ? (const void*)quantize_int8_rows_kernel<BF16, 4>
+                    : (const void*)quantize_int8_rows_kernel<BF16, 8>;
+}
+
 static lbq_status run_quantize_rows(const void* X, int x_dtype, int M, int K, int8_t* xq, float* sx, cudaStream_t st) {
   const int chunks = K / 8;
-  const int vpt = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
-  const int block = std::max(32, (int)align_up((size_t)((chunks + vpt - 1) / vpt), 32));
-  const bool b = x_dtype == LBQ_DTYPE_BF16;
-  const void* fn = vpt == 1   ? (b ? (const void*)quantize_int8_rows_kernel<true, 1> : (const void*)quantize_int8_rows_kernel<false, 1>)
-                   : vpt == 2 ? (b ? (const void*)quantize_int8_rows_kernel<true, 2> : (const void*)quantize_int8_rows_kernel<false, 2>)
-                   : vpt == 4 ? (b ? (const void*)quantize_int8_rows_kernel<true, 4> : (const void*)quantize_int8_rows_kernel<false, 4>)
-                              : (b ? (const void*)quantize_int8_rows_kernel<true, 8> : (const void*)quantize_int8_rows_kernel<false, 8>);
+  const bool bf16 = x_dtype == LBQ_DTYPE_BF16;
   const uint16_t* Xp = static_cast<const uint16_t*>(X);
+  // Enough rows to fill the SMs with warps: a warp per row (up to 2048 values).
+  if (M >= 4 * num_sms() && chunks <= 256) {
+    const void* fn = bf16 ? quantize_rows_kernel<true>((chunks + 31) / 32, true)
+                          : quantize_rows_kernel<false>((chunks + 31) / 32, true);
+    void* args[] = {(void*)&Xp, (void*)&M, (void*)&K, (void*)&xq, (void*)&sx};
+    return launch_kernel_ex(fn, dim3((unsigned)((M + 7) / 8)), dim3(256), 0, st, g_pdl != 0, args,
+                            "quantize_int8_rows launch");
+  }
+  // few rows: as many threads as a row keeps busy; many long rows: bytes in flight per thread
+  const int vpt = chunks > 4096 ? 8 : M >= 4 * num_sms() || chunks > 2048 ? 4 : chunks > 1024 ? 2 : 1;
+  const int block = std::max(32, (int)align_up((size_t)((chunks + vpt - 1) / vpt), 32));
+  const void* fn = bf16 ? quantize_rows_kernel<true>(vpt, false) : quantize_rows_kernel<false>(vpt, false);
   void* args[] = {(void*)&Xp, (void*)&K, (void*)&xq, (void*)&sx};
   return launch_kernel_ex(fn, dim3((unsigned)M), dim3(block), 0, st, g_pdl != 0, args, "quantize_int8_rows launch");
 }
@@ -1745,6 +1810,11 @@ void lbq_debug_lut3_stages(int stages) { g_l3t_stages = (stages >= 1 && stages <
 // Test hook (not in the public header): 1 = LUT3 at M = 2..8 on the skinny
 // kernel instead of the TMA-fed batch kernel (0 = the library's choice).
 void lbq_debug_lut3_batch_off(int on) { g_l3b_off = on ? 1 : 0; }
+
+// Test hook (not in the public header): largest M of the W8A8 product on the
+// CUDA cores (0: none, every M on the tensor cores; -1: the library's choice).
+void lbq_debug_w8a8_fuse(int m) { g_w8_fuse_max = m; }
+void lbq_debug_w8a8_gemv_max(int m) { g_w8_gemv_max = m < 0 ? kW8GvMaxM : std::min(m, kW8GvMaxM); }
 
 // Test hook (not in the public header): prefill stream-K on (1, the library's
 // choice) or off (0: whole tiles, as without a workspace).
@@ -2331,6 +2401,8 @@ lbq_status lbq_w8a8_linear(const void* X, int x_dtype, int M, int K, int N, cons
   int8_t* xq = static_cast<int8_t*>(ws);
   float* sx = reinterpret_cast<float*>(xq + align_up((size_t)M * K, 256));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (w8_gemv_fused(M, K, N))
+    return run_w8a8_gemv(X, x_dtype, nullptr, M, K, N, wq, sw, Y, y_dtype == LBQ_DTYPE_BF16, g_pdl != 0, s);
   if ((st = run_quantize_rows(X, x_dtype, M, K, xq, sx, s)) != LBQ_OK) return st;
   // the product may start (and fetch weights) while the activations are quantised
   return run_w8a8(xq, sx, M, K, N, 1, nullptr, wq, sw, Y, y_dtype == LBQ_DTYPE_BF16, true, s);

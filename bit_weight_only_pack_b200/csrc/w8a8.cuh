@@ -23,15 +23,93 @@ namespace lbq {
 
 // ---------------------------------------------------------------------------- activations
 
-// One block per row of X, the row in registers (VPT chunks of 8 per thread):
-// s = amax / 127 in IEEE FP32 and xq = clamp(rint(x / s), -127, 127), 0 where
-// s = 0. The maximum is taken over the bit patterns of |x| as integers, which
-// order like the values with infinity and NaN above every finite one, so a row
-// with a NaN or infinity gets that scale and codes 0: its products are NaN
-// instead of passing for finite. The quotient is the one of
-// quantize_int8_kernel: the product with RN(1/s) wherever it is at least 2^-14
-// away from a half-integer, the IEEE quotient elsewhere; same codes as the
-// division everywhere.
+// A row's scale from the largest magnitude's bits: s = amax / 127 in IEEE FP32.
+// The maximum is taken over the bit patterns of |x| as integers, which order
+// like the values with infinity and NaN above every finite one, so a row with a
+// NaN or infinity gets that scale and codes 0: its products are NaN instead of
+// passing for finite.
+struct W8Scale {
+  float s, inv;
+  bool zero;   // codes are 0: an all-zero row, or one with an infinity or NaN
+  bool exact;  // 1 / s overflows: every quotient by division
+  __device__ __forceinline__ explicit W8Scale(float amax) {
+    s = __fdiv_rn(amax, 127.0f);
+    inv = __fdiv_rn(1.0f, s);
+    zero = !(s > 0.0f && s <= 3.4028234663852886e38f);
+    exact = !(inv <= 3.4028234663852886e38f);
+  }
+};
+
+// Larger magnitude bits of either half of each word of v.
+__device__ __forceinline__ uint32_t w8_max_bits(uint32_t m2, const uint4& v) {
+  m2 = __vmaxu2(m2, v.x & 0x7FFF7FFFu);
+  m2 = __vmaxu2(m2, v.y & 0x7FFF7FFFu);
+  m2 = __vmaxu2(m2, v.z & 0x7FFF7FFFu);
+  return __vmaxu2(m2, v.w & 0x7FFF7FFFu);
+}
+
+// Codes of 8 values: xq = rint(x / s), ties to even. As in quantize_int8_kernel
+// the product t = RN(x RN(1/s)) decides wherever it is at least 2^-14 from a
+// half-integer; one value closer than that in the eight (about one chunk in a
+// thousand) sends the chunk to the IEEE quotients. |t| < 127.5 because |x| <=
+// amax, so no clamp is needed. Adding 1.5 2^23 rounds t to an integer whose
+// two's complement is the low byte of the sum.
+template <bool BF16>
+__device__ __forceinline__ uint2 w8_codes(const uint4& v, const W8Scale& q) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t b[8];
+  float far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = __fmul_rn(x2f<BF16>((uint16_t)(u[i >> 1] >> (16 * (i & 1)))), q.inv);
+    const float r = __fadd_rn(t, 12582912.0f);
+    far = fmaxf(far, fabsf(__fadd_rn(t, -__fadd_rn(r, -12582912.0f))));
+    b[i] = __float_as_uint(r);
+  }
+  if (q.exact || far > 0.5f - 6.103515625e-05f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      b[i] = (uint32_t)(int)rintf(__fdiv_rn(x2f<BF16>((uint16_t)(u[i >> 1] >> (16 * (i & 1)))), q.s));
+  }
+  if (q.zero) return make_uint2(0u, 0u);
+  return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
+// One warp per row, the row in registers (VPT chunks of 8 per lane): for many
+// rows, where the rows of an SM's warps together are the bytes in flight and no
+// block-wide exchange stops them.
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(256) quantize_int8_rows_warp_kernel(const uint16_t* __restrict__ X, int M, int K,
+                                                                      int8_t* __restrict__ xq,
+                                                                      float* __restrict__ sx) {
+  w8_griddep_launch_dependents();
+  w8_griddep_wait();
+  const int lane = threadIdx.x & 31, chunks = K >> 3;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= M) return;  // whole warps leave
+  const uint4* xr = reinterpret_cast<const uint4*>(X + row * (size_t)K);
+  uint4 v[VPT];
+  uint32_t m2 = 0u;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = lane + i * 32;
+    v[i] = c < chunks ? ld_stream_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) m2 = w8_max_bits(m2, v[i]);
+  const W8Scale q(x2f<BF16>((uint16_t)__reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16))));
+  uint2* out = reinterpret_cast<uint2*>(xq + row * (size_t)K);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = lane + i * 32;
+    if (c < chunks) out[c] = w8_codes<BF16>(v[i], q);
+  }
+  if (lane == 0) sx[row] = q.s;
+}
+
+// One block per row of X, the row in registers (VPT chunks of 8 per thread): for
+// few rows, whose latency counts, and for long ones.
 template <bool BF16, int VPT>
 __global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t* __restrict__ X, int K,
                                                                   int8_t* __restrict__ xq, float* __restrict__ sx) {
@@ -42,54 +120,29 @@ __global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t
   const size_t row = blockIdx.x;
   const uint4* xr = reinterpret_cast<const uint4*>(X + row * (size_t)K);
   uint4 v[VPT];
-  uint32_t m2 = 0u;  // running maxima of the two halves' magnitude bits
+  uint32_t m2 = 0u;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * blockDim.x;
     v[i] = c < chunks ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    m2 = __vmaxu2(m2, v[i].x & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, v[i].y & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, v[i].z & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, v[i].w & 0x7FFF7FFFu);
-  }
-  uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  for (int i = 0; i < VPT; ++i) m2 = w8_max_bits(m2, v[i]);
+  uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
   if (blockDim.x > 32) {
     if ((tid & 31) == 0) warp_max[tid >> 5] = m;
     __syncthreads();
     const uint32_t w = (tid & 31) < (int)(blockDim.x >> 5) ? warp_max[tid & 31] : 0u;
     m = __reduce_max_sync(0xFFFFFFFFu, w);
   }
-  const float s = __fdiv_rn(x2f<BF16>((uint16_t)m), 127.0f);
-  const float inv = __fdiv_rn(1.0f, s);
-  const bool use_inv = inv <= 3.4028234663852886e38f;
-  const bool zero = !(s > 0.0f && s <= 3.4028234663852886e38f);  // all-zero rows; rows with inf or NaN
-  auto code = [&](uint32_t bits) -> uint32_t {
-    const float x = x2f<BF16>((uint16_t)bits);
-    const float t = __fmul_rn(x, inv);
-    float r = rintf(t);
-    if (!use_inv || 0.5f - fabsf(t - r) < 6.103515625e-05f) r = rintf(__fdiv_rn(x, s));
-    r = fminf(fmaxf(r, -127.0f), 127.0f);
-    return zero ? 0u : (uint32_t)(int)r & 0xFFu;
-  };
+  const W8Scale q(x2f<BF16>((uint16_t)m));
   uint2* out = reinterpret_cast<uint2*>(xq + row * (size_t)K);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * blockDim.x;
-    if (c < chunks) {
-      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t o[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o[h] = code(u[2 * h] & 0xFFFFu) | (code(u[2 * h] >> 16) << 8) | (code(u[2 * h + 1] & 0xFFFFu) << 16) |
-               (code(u[2 * h + 1] >> 16) << 24);
-      out[c] = make_uint2(o[0], o[1]);
-    }
+    if (c < chunks) out[c] = w8_codes<BF16>(v[i], q);
   }
-  if (tid == 0) sx[row] = s;
+  if (tid == 0) sx[row] = q.s;
 }
 
 // ---------------------------------------------------------------------------- weights (offline)
@@ -135,6 +188,162 @@ __global__ void __launch_bounds__(256) quantize_int8_weight_kernel(const float* 
       const int nn = blockIdx.x * 32 + i, k = k0 + cx;
       if (nn < N && k < K) wq[(size_t)nn * K + k] = tile[cx][i];
     }
+  }
+}
+
+// ---------------------------------------------------------------------------- product, a few tokens
+
+constexpr int kW8GvWarps = 8;
+constexpr int kW8GvRows = 2;    // channels per warp at a time
+constexpr int kW8GvUnroll = 4;  // 16-byte chunks per lane and channel at a time
+constexpr int kW8GvMaxM = 8;
+constexpr int kW8GvFusedVpt = 8;  // X chunks of 8 per thread that the quantising form keeps in registers
+
+struct W8GemvArgs {
+  const void* X;     // QUANT: [M][K] FP16 / BF16; else int8 codes [M][K]
+  const float* sx;   // [M] (codes only)
+  const int8_t* wq;  // [N][K]
+  const float* sw;   // [N]
+  void* Y;           // [M][N]
+  int M, K, N;
+  int pairs;         // groups of kW8GvRows channels
+  int y_bf16;
+};
+
+// Batch 1..MB on the CUDA cores: HBM-bound on the weights, 4 dp4a per 16 weight
+// bytes and token. A warp takes two channels at a time, lanes take 16-byte chunks of
+// their rows, and the next eight chunks per lane are requested before the last
+// eight are multiplied; the tokens' codes lie in shared memory and serve both
+// channels. Lane sums are integers, so one redux per channel and token joins them.
+// The first weights are requested before anything else: the block then waits for
+// the kernel before (which may write X), and, with QUANT, quantises the tokens
+// itself (every block the same: reading a few KB from L2 costs less than a kernel
+// in front).
+template <int MB, bool QUANT, bool BF16>
+__global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8GemvArgs a) {
+  extern __shared__ __align__(16) uint8_t xs[];  // [MB][K] codes
+  __shared__ uint32_t max_sh[MB][kW8GvWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunks = a.K >> 4;
+  const int steps = (chunks + 32 * kW8GvUnroll - 1) / (32 * kW8GvUnroll);  // per pair
+  w8_griddep_launch_dependents();
+
+  int pair = blockIdx.x * kW8GvWarps + warp, step = 0;  // the next loads
+  const int stride = gridDim.x * kW8GvWarps;
+  uint4 w[kW8GvRows][kW8GvUnroll];
+  auto request = [&] {
+#pragma unroll
+    for (int r = 0; r < kW8GvRows; ++r) {
+      const int n = min(pair * kW8GvRows + r, a.N - 1);
+      const int8_t* row = a.wq + (size_t)n * a.K;
+#pragma unroll
+      for (int u = 0; u < kW8GvUnroll; ++u) {
+        const int c = (step * kW8GvUnroll + u) * 32 + lane;
+        w[r][u] = c < chunks ? ld_stream_v4(row + (size_t)c * 16) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  const bool any = pair < a.pairs;
+  if (any) request();
+
+  float sx[MB];
+  w8_griddep_wait();
+  if constexpr (QUANT) {
+    const int xchunks = a.K >> 3;
+    constexpr int kVpt = kW8GvFusedVpt / MB;
+    uint4 v[MB][kVpt];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.X) + (size_t)m * a.K);
+#pragma unroll
+      for (int i = 0; i < kVpt; ++i) {
+        const int c = tid + i * (kW8GvWarps * 32);
+        v[m][i] = m < a.M && c < xchunks ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      uint32_t m2 = 0u;
+#pragma unroll
+      for (int i = 0; i < kVpt; ++i) m2 = w8_max_bits(m2, v[m][i]);
+      const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
+      if (lane == 0) max_sh[m][warp] = t;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      uint32_t t = 0u;
+#pragma unroll
+      for (int i = 0; i < kW8GvWarps; ++i) t = max(t, max_sh[m][i]);
+      const W8Scale q(x2f<BF16>((uint16_t)t));
+      sx[m] = q.s;
+#pragma unroll
+      for (int i = 0; i < kVpt; ++i) {
+        const int c = tid + i * (kW8GvWarps * 32);
+        if (c < xchunks) *reinterpret_cast<uint2*>(xs + (size_t)m * a.K + (size_t)c * 8) = w8_codes<BF16>(v[m][i], q);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      sx[m] = m < a.M ? __ldg(a.sx + m) : 0.0f;
+      const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.X) + (size_t)m * a.K);
+      for (int c = tid; c < chunks; c += kW8GvWarps * 32)
+        reinterpret_cast<uint4*>(xs + (size_t)m * a.K)[c] = m < a.M ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __syncthreads();
+  if (!any) return;
+
+  int acc[kW8GvRows][MB];
+  for (;;) {
+    const int p = pair, s = step;  // what `w` holds
+    if (s == 0) {
+#pragma unroll
+      for (int r = 0; r < kW8GvRows; ++r)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[r][m] = 0;
+    }
+    if (++step == steps) {
+      step = 0;
+      pair += stride;
+    }
+    uint4 cur[kW8GvRows][kW8GvUnroll];
+#pragma unroll
+    for (int r = 0; r < kW8GvRows; ++r)
+#pragma unroll
+      for (int u = 0; u < kW8GvUnroll; ++u) cur[r][u] = w[r][u];
+    const bool more = pair < a.pairs;
+    if (more) request();
+#pragma unroll
+    for (int u = 0; u < kW8GvUnroll; ++u) {
+      const int c = min((s * kW8GvUnroll + u) * 32 + lane, chunks - 1);  // past the row: weights 0
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const uint4 x = *reinterpret_cast<const uint4*>(xs + (size_t)m * a.K + (size_t)c * 16);
+#pragma unroll
+        for (int r = 0; r < kW8GvRows; ++r) {
+          acc[r][m] = __dp4a((int)cur[r][u].x, (int)x.x, acc[r][m]);
+          acc[r][m] = __dp4a((int)cur[r][u].y, (int)x.y, acc[r][m]);
+          acc[r][m] = __dp4a((int)cur[r][u].z, (int)x.z, acc[r][m]);
+          acc[r][m] = __dp4a((int)cur[r][u].w, (int)x.w, acc[r][m]);
+        }
+      }
+    }
+    if (s == steps - 1) {
+#pragma unroll
+      for (int r = 0; r < kW8GvRows; ++r) {
+        const int n = p * kW8GvRows + r;
+        const float sw = n < a.N ? __ldg(a.sw + n) : 0.0f;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+          const int sum = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);
+          if (lane == r * MB + m && n < a.N && m < a.M)
+            store_out(a.Y, (size_t)m * a.N + n, ((float)sum * sw) * sx[m], a.y_bf16);
+        }
+      }
+    }
+    if (!more) break;
   }
 }
 

@@ -101,6 +101,7 @@ _SIGS = {
     "lbq_moe_combine": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp], _c_int),
     "lbq_moe_combine_grad": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "lbq_debug_w8a8_gemv_max": ([_c_int], None),
+    "lbq_debug_sort_cluster": ([_c_int], None),
     "lbq_debug_force_splits": ([_c_int], None),
     "lbq_debug_force_skinny": ([_c_int], None),
     "lbq_debug_force_tc": ([_c_int], None),
@@ -296,6 +297,11 @@ def lbq_debug_lut3_batch_off(on):
 def lbq_debug_w8a8_gemv_max(m):
     """Test hook: largest M of the W8A8 product on the CUDA cores (-1 = the library's choice)."""
     _lib.lbq_debug_w8a8_gemv_max(int(m))
+
+
+def lbq_debug_sort_cluster(on):
+    """Test hook: every sort on the clustered kernel."""
+    _lib.lbq_debug_sort_cluster(1 if on else 0)
 
 
 def lbq_debug_gemm_stream_k(on):

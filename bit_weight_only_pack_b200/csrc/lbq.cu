@@ -1568,6 +1568,8 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   return p;
 }
 
+// largest pairs x experts of the block-per-expert sort (test hook: 0, the clustered sort always)
+static long long g_sort_work = kSortBlockWork;
 static int g_w8_fuse_max = 2;
 static int g_w8_gemv_max = kW8GvMaxM;  // test hook: largest M on the CUDA-core product
 
@@ -1733,12 +1735,23 @@ static lbq_status check_routed(int T, int top_k, int rows) {
   return LBQ_OK;
 }
 
-// Blocks of 256 threads over `pieces` row pieces.
-static lbq_status pieces_grid(long long pieces, unsigned* grid) {
-  const long long g = (pieces + 255) / 256;
+// Threads per token of the row kernels (a power of two up to the block's 256) for
+// rows of per_row pieces, u pieces per thread and step; and the grid.
+static lbq_status rows_grid(int T, int per_row, int u, int* shift, unsigned* grid) {
+  *shift = 0;
+  while (*shift < 8 && (1LL << *shift) * u < per_row) ++*shift;
+  const long long g = (((long long)T << *shift) + 255) / 256;
   if (g > 0x7FFFFFFFLL) return fail(LBQ_ERR_INVALID_ARG, "too many elements for one launch");
   *grid = (unsigned)g;
   return LBQ_OK;
+}
+
+template <bool BF16>
+static const void* combine_kernel(int n, int top_k) {
+  if (n == 8) return top_k > 4 ? (const void*)moe_combine_kernel<BF16, 8, 8, 1> : (const void*)moe_combine_kernel<BF16, 8, 4, 1>;
+  return n == 4   ? (const void*)moe_combine_kernel<BF16, 4, 4, 2>
+         : n == 2 ? (const void*)moe_combine_kernel<BF16, 2, 4, 4>
+                  : (const void*)moe_combine_kernel<BF16, 1, 4, 4>;
 }
 
 }  // namespace lbq
@@ -1813,6 +1826,8 @@ void lbq_debug_lut3_batch_off(int on) { g_l3b_off = on ? 1 : 0; }
 
 // Test hook (not in the public header): largest M of the W8A8 product on the
 // CUDA cores (0: none, every M on the tensor cores; -1: the library's choice).
+// Test hook (not in the public header): 1 = every sort on the clustered kernel (0 = the library's choice).
+void lbq_debug_sort_cluster(int on) { g_sort_work = on ? 0 : kSortBlockWork; }
 void lbq_debug_w8a8_fuse(int m) { g_w8_fuse_max = m; }
 void lbq_debug_w8a8_gemv_max(int m) { g_w8_gemv_max = m < 0 ? kW8GvMaxM : std::min(m, kW8GvMaxM); }
 
@@ -2432,11 +2447,22 @@ lbq_status lbq_moe_sort(const int32_t* topk_ids, int num_pairs, int num_experts,
   if (num_pairs <= 0 || num_pairs >= (1 << 30) || num_experts <= 0 || num_experts > kW8MaxExperts)
     return fail(LBQ_ERR_INVALID_ARG, "num_pairs=%d (below 2^30) num_experts=%d (1..%d)", num_pairs, num_experts,
                 kW8MaxExperts);
-  const int block = std::min(kSortThreads, std::max(32, (int)align_up((size_t)std::min(num_pairs, kSortThreads), 32)));
   void* args[] = {(void*)&topk_ids, (void*)&num_pairs, (void*)&num_experts, (void*)&row_of_pair, (void*)&pair_of_row,
                   (void*)&offsets};
-  return launch_kernel_ex((const void*)moe_sort_kernel, dim3((unsigned)num_experts), dim3(block), 0,
-                          static_cast<cudaStream_t>(stream), g_pdl != 0, args, "MoE sort launch");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (num_pairs <= kSortBlockPairs && (long long)num_pairs * num_experts <= g_sort_work) {
+    const int v = num_pairs <= 4096 ? 1 : num_pairs <= 8192 ? 2 : 4;
+    const void* fn = v == 1   ? (const void*)moe_sort_block_kernel<1>
+                     : v == 2 ? (const void*)moe_sort_block_kernel<2>
+                              : (const void*)moe_sort_block_kernel<4>;
+    return launch_kernel_ex(fn, dim3((unsigned)num_experts), dim3((unsigned)((num_pairs + v * 128 - 1) / (v * 128) * 32)),
+                            0, s, g_pdl != 0, args, "MoE sort launch");
+  }
+  const int block = num_experts <= 1024 ? kSortThreads : kSortThreads / 2;  // [block / 32][experts] counts
+  const int smem = (block / 32 + 2) * num_experts * (int)sizeof(int);
+  occupancy_for((const void*)moe_sort_kernel, block, smem);  // raises the kernel's dynamic shared-memory limit once
+  return launch_cluster((const void*)moe_sort_kernel, dim3(kSortCluster), kSortCluster, dim3((unsigned)block), smem, s,
+                        g_pdl != 0, args, "MoE sort launch");
 }
 
 lbq_status lbq_moe_permute(const void* X, int row_bytes, int T, int top_k, const int32_t* row_of_pair, int rows,
@@ -2448,17 +2474,16 @@ lbq_status lbq_moe_permute(const void* X, int row_bytes, int T, int top_k, const
   if (!aligned16(X) || !aligned16(row_of_pair) || !aligned16(Xs))
     return fail(LBQ_ERR_INVALID_ARG, "X, row_of_pair and Xs must be 16-byte aligned");
   const int b = row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : row_bytes % 2 == 0 ? 2 : 1;
-  const void* fn = b == 16  ? (const void*)moe_permute_kernel<16>
-                   : b == 8 ? (const void*)moe_permute_kernel<8>
-                   : b == 4 ? (const void*)moe_permute_kernel<4>
-                   : b == 2 ? (const void*)moe_permute_kernel<2>
-                            : (const void*)moe_permute_kernel<1>;
-  int per_row = row_bytes / b;
-  long long pieces = (long long)T * per_row;
+  const void* fn = b == 16  ? (const void*)moe_permute_kernel<16, 1>
+                   : b == 8 ? (const void*)moe_permute_kernel<8, 2>
+                   : b == 4 ? (const void*)moe_permute_kernel<4, 4>
+                   : b == 2 ? (const void*)moe_permute_kernel<2, 4>
+                            : (const void*)moe_permute_kernel<1, 4>;
+  int per_row = row_bytes / b, shift = 0;
   unsigned grid = 0;
-  if ((st = pieces_grid(pieces, &grid)) != LBQ_OK) return st;
-  void* args[] = {(void*)&X, (void*)&pieces, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair, (void*)&rows,
-                  (void*)&Xs};
+  if ((st = rows_grid(T, per_row, b == 16 ? 1 : b == 8 ? 2 : 4, &shift, &grid)) != LBQ_OK) return st;
+  void* args[] = {(void*)&X, (void*)&T, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair, (void*)&rows,
+                  (void*)&Xs, (void*)&shift};
   return launch_kernel_ex(fn, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
                           "MoE permute launch");
 }
@@ -2474,16 +2499,12 @@ lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int
     return fail(LBQ_ERR_INVALID_ARG, "Ys, row_of_pair, weights and out must be 16-byte aligned");
   const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
   const bool b = dtype == LBQ_DTYPE_BF16;
-  const void* fn = n == 8   ? (b ? (const void*)moe_combine_kernel<true, 8> : (const void*)moe_combine_kernel<false, 8>)
-                   : n == 4 ? (b ? (const void*)moe_combine_kernel<true, 4> : (const void*)moe_combine_kernel<false, 4>)
-                   : n == 2 ? (b ? (const void*)moe_combine_kernel<true, 2> : (const void*)moe_combine_kernel<false, 2>)
-                            : (b ? (const void*)moe_combine_kernel<true, 1> : (const void*)moe_combine_kernel<false, 1>);
-  int per_row = H / n;
-  long long pieces = (long long)T * per_row;
+  const void* fn = b ? combine_kernel<true>(n, top_k) : combine_kernel<false>(n, top_k);
+  int per_row = H / n, shift = 0;
   unsigned grid = 0;
-  if ((st = pieces_grid(pieces, &grid)) != LBQ_OK) return st;
-  void* args[] = {(void*)&Ys, (void*)&rows, (void*)&pieces, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
-                  (void*)&weights, (void*)&out};
+  if ((st = rows_grid(T, per_row, n == 8 ? 1 : n == 4 ? 2 : 4, &shift, &grid)) != LBQ_OK) return st;
+  void* args[] = {(void*)&Ys, (void*)&rows, (void*)&T, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
+                  (void*)&weights, (void*)&out, (void*)&shift};
   return launch_kernel_ex(fn, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
                           "MoE combine launch");
 }

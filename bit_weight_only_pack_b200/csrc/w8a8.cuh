@@ -447,6 +447,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 // All threads of the cluster; writes before it are visible after it.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of this block's shared-memory location `addr` in block `rank` of the cluster.

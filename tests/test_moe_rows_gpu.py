@@ -56,11 +56,17 @@ def rounding(torch, ref, t):
 
 @pytest.mark.parametrize("T,top_k,E,dropped", [
     (1, 1, 1, 0), (1, 8, 256, 0), (1, 1, 1, 1.0), (16, 8, 256, 0), (37, 2, 8, 0.3), (300, 1, 3, 0), (333, 3, 2048, 0.1),
-    (5, 4, 2, 0), (2000, 8, 64, 0), (4097, 7, 16, 0.5), (12289, 8, 5, 0),
+    (5, 4, 2, 0), (1024, 4, 3, 0), (1025, 4, 3, 0.01), (2000, 8, 64, 0), (2048, 8, 40, 0), (4097, 7, 16, 0.5), (12289, 8, 5, 0),
 ])
-def test_sort(torch, lbq, T, top_k, E, dropped):
+@pytest.mark.parametrize("cluster", [False, True])
+def test_sort(torch, lbq, T, top_k, E, dropped, cluster):
+    """Both kernels (the library takes the clustered one for many pairs)."""
     ids = routing(np.random.default_rng(T + E), T, top_k, E, dropped)
-    got = [x.cpu().numpy() for x in lbq.moe_sort(torch.from_numpy(ids).cuda(), E)]
+    lbq.lbq_debug_sort_cluster(cluster)
+    try:
+        got = [x.cpu().numpy() for x in lbq.moe_sort(torch.from_numpy(ids).cuda(), E)]
+    finally:
+        lbq.lbq_debug_sort_cluster(False)
     for a, b in zip(got, moe_rows.sort(ids, E)):
         assert np.array_equal(a, b)
 

@@ -114,11 +114,23 @@ def test_quantize_weight_is_bit_exact(torch, lbq, K, N):
 
 @pytest.mark.parametrize("ydt", ["f16", "bf16"])
 @pytest.mark.parametrize("M,K,N", [
-    (1, 16, 1), (1, 4096, 1000), (2, 48, 7), (4, 128, 28), (8, 144, 129), (15, 256, 127), (16, 4112, 1003), (17, 2048, 300),
+    (1, 16, 1), (1, 4096, 1000), (2, 48, 7), (3, 2064, 90), (4, 128, 28), (5, 8208, 40), (8, 144, 129), (8, 14336, 70), (15, 256, 127), (16, 4112, 1003), (17, 2048, 300),
     (31, 512, 64), (33, 1024, 200), (64, 640, 513), (100, 400, 4099), (255, 128, 130), (256, 272, 257), (257, 384, 96),
     (300, 1040, 1003), (513, 256, 2000), (1000, 192, 77), (1025, 64, 3000),
 ])
-def test_gemm_matches_the_integer_sums(torch, lbq, M, K, N, ydt):
+@pytest.mark.parametrize("tensor", [False, True])
+def test_gemm_matches_the_integer_sums(torch, lbq, M, K, N, ydt, tensor):
+    """The library's choice, and every M on the tensor cores."""
+    if tensor and M > 8:
+        pytest.skip("the same kernel")
+    lbq.lbq_debug_w8a8_gemv_max(0 if tensor else -1)
+    try:
+        check_gemm(torch, lbq, M, K, N, ydt)
+    finally:
+        lbq.lbq_debug_w8a8_gemv_max(-1)
+
+
+def check_gemm(torch, lbq, M, K, N, ydt):
     rng = np.random.default_rng(M * 31 + K * 7 + N)
     xq, wq, sx, sw = codes(rng, (M, K)), codes(rng, (N, K)), scales(rng, M), scales(rng, N)
     t = torch.float16 if ydt == "f16" else torch.bfloat16
@@ -131,7 +143,7 @@ def test_gemm_matches_the_integer_sums(torch, lbq, M, K, N, ydt):
     untouched()
 
 
-@pytest.mark.parametrize("M", [1, 20, 300])
+@pytest.mark.parametrize("M", [1, 6, 20, 300])
 def test_gemm_largest_sums_stay_exact(torch, lbq, M):
     """Every product at its largest, 2^14, over the longest K: 2^30."""
     K, N = 65536, 9
@@ -173,7 +185,8 @@ def test_rows_do_not_depend_on_the_batch(torch, lbq):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-@pytest.mark.parametrize("M,K,N", [(1, 4096, 1024), (5, 1040, 333), (7, 14336, 256), (16, 64, 100), (200, 512, 130)])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 1024), (1, 65536, 9), (2, 8192, 77), (2, 8208, 50), (3, 16, 5), (5, 1040, 333), (7, 14336, 256),
+                                   (16, 64, 100), (200, 512, 130)])
 def test_linear_is_the_two_calls(torch, lbq, M, K, N, dt):
     g = torch.Generator(device="cuda").manual_seed(K)
     x = torch.randn((M, K), generator=g, device="cuda").to(torch.float16 if dt == "f16" else torch.bfloat16)

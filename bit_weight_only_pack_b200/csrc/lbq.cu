@@ -1511,15 +1511,18 @@ static W8Plan plan_w8a8(long long M, int K, int N) {
   const double hbm = (double)K * N / 3400.0;  // clocks at 6.4 TB/s
   W8Plan best{};
   double best_cost = 0.0;
-  auto consider = [&](int cg, int ht, int bn, int splits) {
-    const long long m_tiles = (M + bn - 1) / bn, n_tiles = (N + cg * ht - 1) / (cg * ht);
+  // ht: channels per block of a pair; of single blocks as many tiles as given, evenly shared
+  auto consider = [&](int cg, long long n_tiles, int bn, int splits) {
+    const long long m_tiles = (M + bn - 1) / bn;
+    const int ht = cg == 2 ? kW8MaxHt : (int)align_up((size_t)((N + n_tiles - 1) / n_tiles), 8);
     if (m_tiles * n_tiles > 0x3FFFFFFF) return;
     const int sub = w8_sub(ht, bn, cg, K, 1024 + kW8MaxHt * kW8BK);
     double waves = (double)((m_tiles * n_tiles * cg + sms - 1) / sms);
     double once = 2500.0 + 12.0 * bn;
     if (splits > 1) {
       if (waves > 1.0 || m_tiles * n_tiles > w8_max_clusters(splits) || K / kW8BK < splits * sub) return;
-      once += 3500.0;
+      if ((long long)bn * kW8MaxHt * 4 > kW8SmemBudget - 1024) return;  // (the sums lie over ring and slack)
+      once += 3500.0 + 12.0 * bn;
     }
     const double mma = 4.0 * std::max(0.5 * bn, 45.0) + 150.0 / sub, issue = 450.0 / sub;
     const double load = (ht + (double)bn / cg) * kW8BK / 56.0;
@@ -1530,23 +1533,20 @@ static W8Plan plan_w8a8(long long M, int K, int N) {
     }
   };
   const long long m_min = (M + kW8MaxBn - 1) / kW8MaxBn;
-  for (long long mt = m_min; mt <= m_min + m_min / 4 + 1; ++mt) {
+  for (long long mt = m_min; mt <= m_min + m_min / 4 + 4; ++mt) {
     const int bn1 = (int)align_up((size_t)((M + mt - 1) / mt), 16), bn2 = (int)align_up((size_t)((M + mt - 1) / mt), 32);
-    const int full = std::min(kW8MaxHt, (int)align_up((size_t)N, 8));
-    if (N > kW8MaxHt && M > 64) consider(2, kW8MaxHt, bn2, 1);
+    const long long full = (N + kW8MaxHt - 1) / kW8MaxHt, m_tiles = (M + bn1 - 1) / bn1;
+    if (N > kW8MaxHt && M > 64) consider(2, (N + 2 * kW8MaxHt - 1) / (2 * kW8MaxHt), bn2, 1);
     consider(1, full, bn1, 1);
-    const long long m_tiles = (M + bn1 - 1) / bn1;
-    const long long w0 = ((long long)((N + kW8MaxHt - 1) / kW8MaxHt) * m_tiles + sms - 1) / sms;
-    if (w0 * sms >= m_tiles) {  // ht that fills w0 waves
-      const long long nt = w0 * sms / m_tiles;
-      consider(1, (int)std::min<long long>(full, align_up((size_t)((N + nt - 1) / nt), 8)), bn1, 1);
-    }
-    if (bn1 <= kW8MaxSplitBn && m_tiles == 1)
-      for (int s = 2; s <= kW8MaxSplits; s *= 2) {
-        const int nt = w8_max_clusters(s);
-        if (nt > 0)
-          consider(1, (int)std::min<long long>(full, align_up((size_t)((N + nt - 1) / nt), 8)), bn1, s);
+    const long long w0 = (full * m_tiles + sms - 1) / sms;  // waves of full tiles, filled
+    consider(1, std::min<long long>(N, std::max(full, w0 * sms / m_tiles)), bn1, 1);
+    for (int s = 2; s <= kW8MaxSplits; s *= 2) {
+      const long long nt = w8_max_clusters(s) / m_tiles;
+      if (nt >= full) {
+        consider(1, full, bn1, s);
+        consider(1, std::min<long long>(N, nt), bn1, s);
       }
+    }
   }
   return best;
 }
@@ -1564,7 +1564,7 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   p.ht = std::min(kW8MaxHt, (int)align_up((size_t)((N + p.cg * p.n_tiles - 1) / (p.cg * p.n_tiles)), 8));
   p.n_tiles = (N + p.cg * p.ht - 1) / (p.cg * p.ht);
   p.splits = 1;
-  p.sub = w8_sub(p.ht, p.bn, p.cg, K, 1024 + kW8MaxHt * kW8BK + (E + 1) * (int)sizeof(int));
+  p.sub = w8_sub(p.ht, p.bn, p.cg, K, 1024 + kW8MaxHt * kW8BK + 2 * (E + 1) * (int)sizeof(int));
   return p;
 }
 
@@ -1661,7 +1661,7 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
   if (!ok) return fail(LBQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the W8A8 operands");
 
   // alignment, the slack behind the ring, and the routed form's tile counts
-  const int extra = 1024 + kW8MaxHt * kW8BK + (offsets ? (E + 1) * (int)sizeof(int) : 0);
+  const int extra = 1024 + kW8MaxHt * kW8BK + (offsets ? 2 * (E + 1) * (int)sizeof(int) : 0);
   a.stages = std::min(kW8MaxStages, (kW8SmemBudget - extra) / a.stage_bytes);
   const int smem = a.stages * a.stage_bytes + extra;
   const void* fn = p.cg == 2 ? (const void*)w8a8_gemm_kernel<2> : (const void*)w8a8_gemm_kernel<1>;

@@ -30,10 +30,10 @@ constexpr long long kSortBlockWork = 1 << 24; // ... and pairs times experts
 // 3.6 against 5.6, 4096 and 1024 5.6 against 8.2, 8192 and 2048 12.1 against 16.0;
 // 32768 and 256 10.2 against 8.3, 32768 and 8 9.4 against 6.4.
 template <int V>
-__global__ void __launch_bounds__(kSortThreads) moe_sort_block_kernel(const int32_t* __restrict__ ids, int P, int E,
-                                                                      int32_t* __restrict__ row_of_pair,
-                                                                      int32_t* __restrict__ pair_of_row,
-                                                                      int32_t* __restrict__ offsets) {
+__global__ void __launch_bounds__(kSortThreads) moe_sort_block_kernel(const int32_t* ids, int P, int E,
+                                                                      int32_t* row_of_pair,
+                                                                      int32_t* pair_of_row,
+                                                                      int32_t* offsets) {
   __shared__ int eq_sh[32], lt_sh[32];
   w8_griddep_launch_dependents();
   w8_griddep_wait();
@@ -48,9 +48,9 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_block_kernel(const int3
     if (p + 3 < P) {
       id[v] = ld_nc_v4(ids + p);
     } else {
-      if (p < P) id[v].x = (uint32_t)__ldg(ids + p);
-      if (p + 1 < P) id[v].y = (uint32_t)__ldg(ids + p + 1);
-      if (p + 2 < P) id[v].z = (uint32_t)__ldg(ids + p + 2);
+      if (p < P) id[v].x = (uint32_t)*(ids + p);
+      if (p + 1 < P) id[v].y = (uint32_t)*(ids + p + 1);
+      if (p + 2 < P) id[v].z = (uint32_t)*(ids + p + 2);
     }
   }
   int eq = 0, lt = 0;
@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_block_kernel(const int3
 // same id by their rank among them). Time grows with the pairs, not with the
 // experts.
 // Dynamic shared memory: [warps][E] counts, [E] totals of the block, [E] bases.
-__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* __restrict__ ids, int P, int E,
-                                                                int32_t* __restrict__ row_of_pair,
-                                                                int32_t* __restrict__ pair_of_row,
-                                                                int32_t* __restrict__ offsets) {
+__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* ids, int P, int E,
+                                                                int32_t* row_of_pair,
+                                                                int32_t* pair_of_row,
+                                                                int32_t* offsets) {
   extern __shared__ int sort_sm[];
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* _
   int* mine = count + warp * E;
 #pragma unroll 4
   for (int p = p0 + lane; p < p1; p += 32) {
-    const uint32_t id = (uint32_t)__ldg(ids + p);
+    const uint32_t id = (uint32_t)*(ids + p);
     if (id < (uint32_t)E) atomicAdd(&mine[id], 1);
   }
   __syncthreads();
@@ -186,11 +186,11 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* _
 
   // (match.any takes some 70 clocks of the SM per warp; log2 E votes are cheaper)
   const int bits = E > 1 ? 32 - __clz(E - 1) : 0;
-  uint32_t next = p0 + lane < p1 ? (uint32_t)__ldg(ids + p0 + lane) : 0xFFFFFFFFu;
+  uint32_t next = p0 + lane < p1 ? (uint32_t)*(ids + p0 + lane) : 0xFFFFFFFFu;
   for (int p = p0; p < p1; p += 32) {
     const bool in = p + lane < p1;
     const uint32_t id = next;
-    next = p + 32 + lane < p1 ? (uint32_t)__ldg(ids + p + 32 + lane) : 0xFFFFFFFFu;
+    next = p + 32 + lane < p1 ? (uint32_t)*(ids + p + 32 + lane) : 0xFFFFFFFFu;
     uint32_t same = __ballot_sync(0xFFFFFFFFu, id < (uint32_t)E);  // lanes with this lane's id, bit by bit
     for (int b = 0; b < bits; ++b) {
       const uint32_t set = __ballot_sync(0xFFFFFFFFu, (id >> b) & 1u);
@@ -223,9 +223,9 @@ template <> struct RowVec<1> { using T = uint8_t; };
 // step, so that narrow pieces (rows that 16 bytes do not divide) still have
 // several loads in flight.
 template <int B, int U>
-__global__ void __launch_bounds__(256) moe_permute_kernel(const void* __restrict__ X, int T, int per_row, int top_k,
-                                                          const int32_t* __restrict__ row_of_pair, int rows,
-                                                          void* __restrict__ Xs, int shift) {
+__global__ void __launch_bounds__(256) moe_permute_kernel(const void* X, int T, int per_row, int top_k,
+                                                          const int32_t* row_of_pair, int rows,
+                                                          void* Xs, int shift) {
   using V = typename RowVec<B>::T;
   w8_griddep_launch_dependents();
   w8_griddep_wait();
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const void* __restrict
     for (int u = 0; u < U; ++u)
       if (c0 + u * lanes < per_row) v[u] = x[c0 + u * lanes];
     for (int j = 0; j < top_k; ++j) {
-      const int r = __ldg(rp + j);
+      const int r = *(rp + j);
       if (r < 0 || r >= rows) continue;
       V* y = static_cast<V*>(Xs) + (size_t)r * per_row + c0;
 #pragma unroll
@@ -271,9 +271,9 @@ __device__ __forceinline__ typename RowVec<2 * N>::T pack_row(const float (&f)[N
 // token's top_k rows summed in FP32, j ascending, rounded once, J rows times U
 // pieces in flight per thread. weights null: 1.
 template <bool BF16, int N, int J, int U>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const void* __restrict__ Y, int rows, int T, int per_row,
-                                                          int top_k, const int32_t* __restrict__ row_of_pair,
-                                                          const float* __restrict__ weights, void* __restrict__ out,
+__global__ void __launch_bounds__(256) moe_combine_kernel(const void* Y, int rows, int T, int per_row,
+                                                          int top_k, const int32_t* row_of_pair,
+                                                          const float* weights, void* out,
                                                           int shift) {
   using V = typename RowVec<2 * N>::T;
   w8_griddep_launch_dependents();
@@ -293,13 +293,13 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const void* __restrict
       bool use[J];
 #pragma unroll
       for (int i = 0; i < J; ++i) {
-        const int r = j0 + i < top_k ? __ldg(row_of_pair + t * top_k + j0 + i) : -1;
+        const int r = j0 + i < top_k ? *(row_of_pair + t * top_k + j0 + i) : -1;
         use[i] = r >= 0 && r < rows;
         const V* y = static_cast<const V*>(Y) + (size_t)(use[i] ? r : 0) * per_row + c0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (use[i] && c0 + u * lanes < per_row) v[i][u] = y[u * lanes];
-        w[i] = use[i] && weights ? __ldg(weights + t * top_k + j0 + i) : 1.0f;
+        w[i] = use[i] && weights ? *(weights + t * top_k + j0 + i) : 1.0f;
       }
 #pragma unroll
       for (int i = 0; i < J; ++i)
@@ -325,11 +325,11 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const void* __restrict
 // in a fixed order. dY may be Y (a thread reads a place before it writes it), so
 // neither is declared restrict.
 template <bool BF16, int N>
-__global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* __restrict__ dout, const void* Y, int rows,
+__global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* dout, const void* Y, int rows,
                                                                int per_row, int top_k,
-                                                               const int32_t* __restrict__ row_of_pair,
-                                                               const float* __restrict__ weights, void* dY,
-                                                               float* __restrict__ dweights) {
+                                                               const int32_t* row_of_pair,
+                                                               const float* weights, void* dY,
+                                                               float* dweights) {
   using V = typename RowVec<2 * N>::T;
   __shared__ float red[4][8];
   w8_griddep_launch_dependents();
@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* __res
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = j0 + u;
-      r[u] = j < top_k ? __ldg(row_of_pair + t * top_k + j) : -1;
+      r[u] = j < top_k ? *(row_of_pair + t * top_k + j) : -1;
       if (r[u] >= rows) r[u] = -1;
-      w[u] = r[u] >= 0 ? __ldg(weights + t * top_k + j) : 0.0f;
+      w[u] = r[u] >= 0 ? *(weights + t * top_k + j) : 0.0f;
       dot[u] = 0.0f;
     }
     for (int c = tid; c < per_row; c += blockDim.x) {

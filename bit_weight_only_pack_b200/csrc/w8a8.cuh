@@ -11,6 +11,10 @@
 //    lanes) and the tokens its N, so a few tokens cost a narrow MMA instead of
 //    a padded one and the weights, the large operand of a decode step, are
 //    streamed once whatever the batch.
+//
+// What a kernel reads after its griddepcontrol.wait is read by plain loads from
+// pointers without __restrict__ (or by volatile asm): the compiler may move a
+// __ldg, or a load it takes for one, up across the wait.
 #pragma once
 
 #include "common.cuh"
@@ -80,9 +84,9 @@ __device__ __forceinline__ uint2 w8_codes(const uint4& v, const W8Scale& q) {
 // rows, where the rows of an SM's warps together are the bytes in flight and no
 // block-wide exchange stops them.
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(256) quantize_int8_rows_warp_kernel(const uint16_t* __restrict__ X, int M, int K,
-                                                                      int8_t* __restrict__ xq,
-                                                                      float* __restrict__ sx) {
+__global__ void __launch_bounds__(256) quantize_int8_rows_warp_kernel(const uint16_t* X, int M, int K,
+                                                                      int8_t* xq,
+                                                                      float* sx) {
   w8_griddep_launch_dependents();
   w8_griddep_wait();
   const int lane = threadIdx.x & 31, chunks = K >> 3;
@@ -111,8 +115,8 @@ __global__ void __launch_bounds__(256) quantize_int8_rows_warp_kernel(const uint
 // One block per row of X, the row in registers (VPT chunks of 8 per thread): for
 // few rows, whose latency counts, and for long ones.
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t* __restrict__ X, int K,
-                                                                  int8_t* __restrict__ xq, float* __restrict__ sx) {
+__global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t* X, int K,
+                                                                  int8_t* xq, float* sx) {
   __shared__ uint32_t warp_max[32];
   w8_griddep_launch_dependents();
   w8_griddep_wait();
@@ -150,8 +154,8 @@ __global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t
 // FP32 weight [K][N] -> codes [N][K] and a scale per channel, by the same rule.
 // Block = 32 channels x 8 k rows; pass 1 the channels' maxima, pass 2 the codes,
 // turned through a 32 x 32 tile so that both sides are read and written in rows.
-__global__ void __launch_bounds__(256) quantize_int8_weight_kernel(const float* __restrict__ W, int K, int N,
-                                                                   int8_t* __restrict__ wq, float* __restrict__ sw) {
+__global__ void __launch_bounds__(256) quantize_int8_weight_kernel(const float* W, int K, int N,
+                                                                   int8_t* wq, float* sw) {
   __shared__ float red[8][32];
   __shared__ int8_t tile[32][33];
   const int cx = threadIdx.x & 31, ky = threadIdx.x >> 5;
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
   } else {
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
-      sx[m] = m < a.M ? __ldg(a.sx + m) : 0.0f;
+      sx[m] = m < a.M ? *(a.sx + m) : 0.0f;
       const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.X) + (size_t)m * a.K);
       for (int c = tid; c < chunks; c += kW8GvWarps * 32)
         reinterpret_cast<uint4*>(xs + (size_t)m * a.K)[c] = m < a.M ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
 #pragma unroll
       for (int r = 0; r < kW8GvRows; ++r) {
         const int n = p * kW8GvRows + r;
-        const float sw = n < a.N ? __ldg(a.sw + n) : 0.0f;
+        const float sw = n < a.N ? *(a.sw + n) : 0.0f;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
           const int sum = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);
@@ -355,7 +359,6 @@ constexpr int kW8MaxBn = 256;     // tokens per tile (MMA N)
 constexpr int kW8MaxStages = 16;
 constexpr int kW8Threads = 192;   // TMA producer, MMA issuer, four epilogue warps
 constexpr int kW8MaxSplits = 8;   // blocks that share one tile's K (one cluster)
-constexpr int kW8MaxSplitBn = 64; // ... of at most this many tokens
 constexpr int kW8MaxExperts = 2048;
 constexpr int kW8MaxK = 65536;        // 2^16 products of at most 2^14: the sum stays in int32
 constexpr int kW8SmemBudget = 222 * 1024;  // dynamic; barriers and the epilogue's scales take the rest of 227 KB
@@ -461,6 +464,12 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ int4 ld_cluster4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
@@ -508,18 +517,25 @@ struct W8Tile {
   int n0, nh, m0, mh, e;
 };
 
-// Tile `t` of the call. Dense: bands of token tiles (stream_k.cuh). Routed:
-// start[e] = token tiles of the experts before e (shared memory), channels
-// inner, so an expert's tiles are neighbours.
+// Tile `t` of the call. Dense: bands of token tiles (stream_k.cuh); with CG = 1
+// the channels are shared out evenly, tiles of at most ht (a tile's copy may take
+// in a few rows of the next, which that one reads at the same time anyway).
+// Routed: start[e] = token tiles of the experts before e and first[e] = the first
+// row of e (shared memory), channels inner, so an expert's tiles are neighbours.
 template <int CG>
-__device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, int t, int rank) {
+__device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, const int* first, int t, int rank) {
   W8Tile w;
-  int nt, mt;
+  int nt = t, mt = 0;
   if (a.offsets == nullptr) {
-    sk_tile_coords(t, a.n_tiles, a.m_tiles, nt, mt);
+    if (a.m_tiles > 1) sk_tile_coords(t, a.n_tiles, a.m_tiles, nt, mt);
     w.e = 0;
     w.m0 = mt * a.bn;
     w.mh = min(a.bn, a.M - w.m0);
+    if (CG == 1) {
+      w.n0 = (int)((long long)nt * a.N / a.n_tiles);
+      w.nh = (int)((long long)(nt + 1) * a.N / a.n_tiles) - w.n0;
+      return w;
+    }
   } else {
     mt = t / a.n_tiles;
     nt = t - mt * a.n_tiles;
@@ -530,9 +546,8 @@ __device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, i
       else hi = mid;
     }
     w.e = lo;
-    const int first = min(max(__ldg(a.offsets + lo), 0), a.M), end = min(max(__ldg(a.offsets + lo + 1), 0), a.M);
-    w.m0 = first + (mt - start[lo]) * a.bn;
-    w.mh = min(a.bn, end - w.m0);
+    w.m0 = first[lo] + (mt - start[lo]) * a.bn;
+    w.mh = min(a.bn, first[lo + 1] - w.m0);
   }
   w.n0 = (CG * nt + (CG == 2 ? rank : 0)) * a.ht;
   w.nh = max(0, min(a.ht, a.N - w.n0));
@@ -555,16 +570,16 @@ __device__ __forceinline__ int w8_x_rows(const W8a8Args& a, int map) {
   return a.offsets == nullptr ? a.bn / CG : 16 << map;
 }
 
-// start[0 .. E] of the routed form, by the whole block (contiguous ranges of
-// experts per thread, a warp scan, then the warps' totals).
-__device__ __forceinline__ void w8_expert_tiles(const W8a8Args& a, int* start) {
+// start[0 .. E] and first[0 .. E] of the routed form, by the whole block
+// (contiguous ranges of experts per thread, a warp scan, then the warps' totals).
+// Offsets outside the rows are clamped to them.
+__device__ __forceinline__ void w8_expert_tiles(const W8a8Args& a, int* start, int* first) {
   __shared__ int warp_sum[kW8Threads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int e = tid; e <= a.E; e += kW8Threads) first[e] = min(max(*(a.offsets + e), 0), a.M);
+  __syncthreads();
   const int per = (a.E + kW8Threads - 1) / kW8Threads, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
-  auto tiles_of = [&](int e) {
-    const int first = min(max(__ldg(a.offsets + e), 0), a.M), end = min(max(__ldg(a.offsets + e + 1), 0), a.M);
-    return end > first ? (end - first + a.bn - 1) / a.bn : 0;
-  };
+  auto tiles_of = [&](int e) { return (max(first[e + 1] - first[e], 0) + a.bn - 1) / a.bn; };
   int mine = 0;
   for (int e = e0; e < e1; ++e) mine += tiles_of(e);
   int incl = mine;
@@ -666,7 +681,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int split_ok;
   uint8_t* ring = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
-  int* start = reinterpret_cast<int*>(ring + (size_t)a.stages * a.stage_bytes + kW8MaxHt * kW8BK);
+  int* start = reinterpret_cast<int*>(ring + (size_t)a.stages * a.stage_bytes + kW8MaxHt * kW8BK);  // routed only
+  int* first = start + a.E + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool split = CG == 1 && a.splits > 1;
@@ -692,7 +708,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   }
   if (a.offsets != nullptr) {
     w8_griddep_wait();  // the offsets come from a kernel before
-    w8_expert_tiles(a, start);
+    w8_expert_tiles(a, start, first);
   }
   tc_fence_before();
   __syncthreads();
@@ -731,7 +747,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     // writes the activations has ended
     int pre = 0;
     for (int tile = unit; tile < total && pre < a.stages; tile += units) {
-      const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+      const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
       const int xrows = w8_x_rows<CG>(a, w8_x_map<CG>(a, w.mh));
       for (int ks = ks0; ks < ks1 && pre < a.stages; ++ks, ++pre) load_w(w, xrows, ks, pre);
     }
@@ -740,7 +756,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     int it = 0;
     bool ok = true;
     for (int tile = unit; tile < total && ok; tile += units) {
-      const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+      const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
       const int map = w8_x_map<CG>(a, w.mh), xrows = w8_x_rows<CG>(a, map);
       const int x0 = w.m0 + (CG == 2 ? rank * (w8_mma_n<2>(w.mh) / 2) : 0);  // a pair: half of the MMA's N each
       for (int ks = ks0; ks < ks1; ++ks, ++it) {
@@ -770,7 +786,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       int t_iter = 0;
       bool ok = true;
       for (int tile = unit; tile < total && ok; tile += units, ++t_iter) {
-        const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+        const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
         const uint32_t idesc = umma_idesc_i8(128 * CG, w8_mma_n<CG>(w.mh));
         const int ai = t_iter & 1;
         const uint32_t d = tmem + (uint32_t)(ai * a.acc_stride);
@@ -813,13 +829,13 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     float* sxs = sx_sh[warp - 2];
     int t_iter = 0;
     for (int tile = unit; tile < total; tile += units, ++t_iter) {
-      const W8Tile w = w8_tile<CG>(a, start, tile, rank);
+      const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
       const int ai = t_iter & 1;
       const int r = 32 * q + lane;  // channel within the block's part of the tile
       const bool row_ok = r < w.nh;
-      const float sw = row_ok ? __ldg(a.sw + (size_t)w.e * a.N + w.n0 + r) : 0.0f;
+      const float sw = row_ok ? *(a.sw + (size_t)w.e * a.N + w.n0 + r) : 0.0f;
       __syncwarp();  // the last tile's scales have been read
-      for (int j = lane; j < w.mh; j += 32) sxs[j] = __ldg(a.sx + w.m0 + j);
+      for (int j = lane; j < w.mh; j += 32) sxs[j] = *(a.sx + w.m0 + j);
       __syncwarp();
       if (!mbar_wait_sleep(&d_full[ai], (t_iter >> 1) & 1)) break;
       tc_fence_after();
@@ -854,21 +870,35 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   if (split) {
     cluster_sync();  // every block's sums are in place
     if (warp >= 2 && unit < total) {
-      const W8Tile w = w8_tile<CG>(a, start, unit, rank);
-      const int r = tid - 64;
+      const W8Tile w = w8_tile<CG>(a, start, first, unit, rank);
       bool ok = true;
       for (int c = 0; c < a.splits; ++c) ok = ok && ld_cluster(cluster_addr(smem_u32(&split_ok), (uint32_t)c)) != 0;
-      if (ok && r < w.nh) {
-        const float sw = __ldg(a.sw + (size_t)w.e * a.N + w.n0 + r);
-        const uint32_t part = smem_u32(ring) + 4u * (uint32_t)r;
-        for (int t = rank; t < w.mh; t += a.splits) {
-          int sum = 0;
+      // lane = four channels, warp = a token at a time of every splits-th
+      const int c0 = (lane << 2), left = w.nh - c0;
+      if (ok && left > 0) {
+        float sw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sw[i] = i < left ? *(a.sw + (size_t)w.e * a.N + w.n0 + c0 + i) : 0.0f;
+        const uint32_t part = smem_u32(ring) + 4u * (uint32_t)c0;
+#pragma unroll 2
+        for (int t = rank + (warp - 2) * a.splits; t < w.mh; t += 4 * a.splits) {
+          int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll
           for (int c = 0; c < kW8MaxSplits; ++c)
-            if (c < a.splits) sum += ld_cluster(cluster_addr(part + (uint32_t)(t * kW8MaxHt * 4), (uint32_t)c));
-          const float f = ((float)sum * sw) * __ldg(a.sx + w.m0 + t);
-          static_cast<uint16_t*>(a.Y)[(size_t)(w.m0 + t) * a.N + w.n0 + r] =
-              a.y_bf16 ? w8_round<true>(f) : w8_round<false>(f);
+            if (c < a.splits) {
+              const int4 v = ld_cluster4(cluster_addr(part + (uint32_t)(t * kW8MaxHt * 4), (uint32_t)c));
+              sum.x += v.x;
+              sum.y += v.y;
+              sum.z += v.z;
+              sum.w += v.w;
+            }
+          const float sx = *(a.sx + w.m0 + t);
+          const float f[4] = {((float)sum.x * sw[0]) * sx, ((float)sum.y * sw[1]) * sx, ((float)sum.z * sw[2]) * sx,
+                              ((float)sum.w * sw[3]) * sx};
+          uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + t) * a.N + w.n0 + c0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < left) y[i] = a.y_bf16 ? w8_round<true>(f[i]) : w8_round<false>(f[i]);
         }
       }
       __syncwarp();

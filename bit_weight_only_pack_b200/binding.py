@@ -101,6 +101,8 @@ _SIGS = {
     "lbq_moe_combine": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp], _c_int),
     "lbq_moe_combine_grad": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "lbq_debug_w8a8_gemv_max": ([_c_int], None),
+    "lbq_debug_w8a8_plan": ([_c_int, _c_int, _c_int, _c_int], None),
+    "lbq_debug_w8a8_planned": ([_c_int, _c_int, _c_int, ctypes.POINTER(_c_int)], None),
     "lbq_debug_sort_cluster": ([_c_int], None),
     "lbq_debug_force_splits": ([_c_int], None),
     "lbq_debug_force_skinny": ([_c_int], None),
@@ -297,6 +299,18 @@ def lbq_debug_lut3_batch_off(on):
 def lbq_debug_w8a8_gemv_max(m):
     """Test hook: largest M of the W8A8 product on the CUDA cores (-1 = the library's choice)."""
     _lib.lbq_debug_w8a8_gemv_max(int(m))
+
+
+def lbq_debug_w8a8_plan(cg, n_tiles=1, bn=16, splits=1):
+    """Test hook: force the dense W8A8 tensor-core plan (cg = 0: the library's choice)."""
+    _lib.lbq_debug_w8a8_plan(cg, n_tiles, bn, splits)
+
+
+def lbq_debug_w8a8_planned(M, K, N):
+    """Test hook: (cg, ht, n_tiles, bn, m_tiles, splits, sub) of the dense W8A8 plan."""
+    out = (_c_int * 7)()
+    _lib.lbq_debug_w8a8_planned(M, K, N, out)
+    return tuple(out)
 
 
 def lbq_debug_sort_cluster(on):

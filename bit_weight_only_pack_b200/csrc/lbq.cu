@@ -1489,6 +1489,16 @@ static int w8_max_clusters(int splits) {
   return cached[splits];
 }
 
+// Channels are shared out to tiles in steps of this many (what divides N, up to 4).
+static int w8_unit(int N) { return N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1; }
+
+// Shared memory besides the ring: alignment, the slack behind it, and the sums of
+// splits (tokens rounded up to whole groups) or the routed form's tables.
+static int w8_extra(int bn, int splits, int E) {
+  return 1024 + kW8MaxHt * kW8BK + (splits > 1 ? (bn + splits) * kW8MaxHt * (int)sizeof(int) : 0) +
+         (E ? 2 * (E + 1) * (int)sizeof(int) : 0);
+}
+
 // Whole k-blocks per ring stage: as many as leave three stages (issuing a stage
 // costs its warps some 400 clocks whatever its size), at most four.
 static int w8_sub(int ht, int bn, int cg, int K, int extra) {
@@ -1505,47 +1515,68 @@ static int w8_sub(int ht, int bn, int cg, int K, int extra) {
 // so that the tiles fill the SMs (any multiple of 8 works), or few channels leave
 // SMs over and the blocks of a cluster share a tile's K. Many tokens: pairs of
 // blocks with 256 channels, and bn is cut if that saves a part-filled wave.
+static W8Plan g_w8_force{};  // test hook: the dense plan's cg, n_tiles, bn and splits (cg 0: the library's choice)
+
+static W8Plan w8_plan_of(int cg, long long n_tiles, int bn, int splits, long long M, int K, int N) {
+  const int unit = w8_unit(N);
+  W8Plan p{};
+  p.cg = cg;
+  p.bn = bn;
+  p.splits = splits;
+  p.n_tiles = (int)n_tiles;
+  p.m_tiles = (int)((M + bn - 1) / bn);
+  p.ht = cg == 2 ? kW8MaxHt : (int)align_up((size_t)unit * (((N + unit - 1) / unit + n_tiles - 1) / n_tiles), 8);
+  p.sub = w8_sub(p.ht, bn, cg, K, w8_extra(bn, splits, 0));
+  return p;
+}
+
+// Whether the kernel can run this plan.
+static bool w8_plan_ok(const W8Plan& p, int K, int N) {
+  if (p.ht > kW8MaxHt || p.bn > kW8MaxBn || p.bn % (16 * p.cg) || (long long)p.m_tiles * p.n_tiles > 0x3FFFFFFF) return false;
+  if ((long long)p.cg * p.ht * p.n_tiles < N || p.n_tiles < 1) return false;
+  if (p.splits == 1) return true;
+  const long long tiles = (long long)p.m_tiles * p.n_tiles;
+  return p.cg == 1 && p.bn <= kW8MaxSplitBn && tiles <= w8_max_clusters(p.splits) && K / kW8BK >= p.splits * p.sub;
+}
+
 static W8Plan plan_w8a8(long long M, int K, int N) {
+  if (g_w8_force.cg) {
+    const W8Plan& f = g_w8_force;
+    const W8Plan p = w8_plan_of(f.cg, f.n_tiles, f.bn, f.splits, M, K, N);
+    return w8_plan_ok(p, K, N) ? p : W8Plan{};
+  }
   const int sms = num_sms();
   const double kb = (K + kW8BK - 1) / kW8BK;
   const double hbm = (double)K * N / 3400.0;  // clocks at 6.4 TB/s
   W8Plan best{};
   double best_cost = 0.0;
-  // ht: channels per block of a pair; of single blocks as many tiles as given, evenly shared
   auto consider = [&](int cg, long long n_tiles, int bn, int splits) {
-    const long long m_tiles = (M + bn - 1) / bn;
-    const int ht = cg == 2 ? kW8MaxHt : (int)align_up((size_t)((N + n_tiles - 1) / n_tiles), 8);
-    if (m_tiles * n_tiles > 0x3FFFFFFF) return;
-    const int sub = w8_sub(ht, bn, cg, K, 1024 + kW8MaxHt * kW8BK);
-    double waves = (double)((m_tiles * n_tiles * cg + sms - 1) / sms);
+    const W8Plan p = w8_plan_of(cg, n_tiles, bn, splits, M, K, N);
+    if (!w8_plan_ok(p, K, N)) return;
+    const double waves = (double)(((long long)p.m_tiles * p.n_tiles * cg + sms - 1) / sms);
     double once = 2500.0 + 12.0 * bn;
-    if (splits > 1) {
-      if (waves > 1.0 || m_tiles * n_tiles > w8_max_clusters(splits) || K / kW8BK < splits * sub) return;
-      if ((long long)bn * kW8MaxHt * 4 > kW8SmemBudget - 1024) return;  // (the sums lie over ring and slack)
-      once += 3500.0 + 12.0 * bn;
-    }
-    const double mma = 4.0 * std::max(0.5 * bn, 45.0) + 150.0 / sub, issue = 450.0 / sub;
-    const double load = (ht + (double)bn / cg) * kW8BK / 56.0;
+    if (splits > 1) once += 2500.0 + 12.0 * bn;
+    const double mma = 4.0 * std::max(0.5 * bn, 45.0) + 150.0 / p.sub, issue = 450.0 / p.sub;
+    const double load = (p.ht + (double)bn / cg) * kW8BK / 56.0;
     const double cost = std::max(hbm, waves * std::ceil(kb / splits) * std::max(std::max(mma, issue), load)) + once;
     if (best.bn == 0 || cost < best_cost) {
       best_cost = cost;
-      best = W8Plan{cg, ht, (int)n_tiles, bn, (int)m_tiles, splits, sub};
+      best = p;
     }
   };
+  const long long units = (N + w8_unit(N) - 1) / w8_unit(N), full = (N + kW8MaxHt - 1) / kW8MaxHt;
   const long long m_min = (M + kW8MaxBn - 1) / kW8MaxBn;
   for (long long mt = m_min; mt <= m_min + m_min / 4 + 4; ++mt) {
     const int bn1 = (int)align_up((size_t)((M + mt - 1) / mt), 16), bn2 = (int)align_up((size_t)((M + mt - 1) / mt), 32);
-    const long long full = (N + kW8MaxHt - 1) / kW8MaxHt, m_tiles = (M + bn1 - 1) / bn1;
+    const long long m_tiles = (M + bn1 - 1) / bn1;
     if (N > kW8MaxHt && M > 64) consider(2, (N + 2 * kW8MaxHt - 1) / (2 * kW8MaxHt), bn2, 1);
     consider(1, full, bn1, 1);
     const long long w0 = (full * m_tiles + sms - 1) / sms;  // waves of full tiles, filled
-    consider(1, std::min<long long>(N, std::max(full, w0 * sms / m_tiles)), bn1, 1);
+    consider(1, std::min(units, std::max(full, w0 * sms / m_tiles)), bn1, 1);
     for (int s = 2; s <= kW8MaxSplits; s *= 2) {
       const long long nt = w8_max_clusters(s) / m_tiles;
-      if (nt >= full) {
-        consider(1, full, bn1, s);
-        consider(1, std::min<long long>(N, nt), bn1, s);
-      }
+      consider(1, full, bn1, s);
+      consider(1, std::min(units, nt), bn1, s);
     }
   }
   return best;
@@ -1564,7 +1595,7 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   p.ht = std::min(kW8MaxHt, (int)align_up((size_t)((N + p.cg * p.n_tiles - 1) / (p.cg * p.n_tiles)), 8));
   p.n_tiles = (N + p.cg * p.ht - 1) / (p.cg * p.ht);
   p.splits = 1;
-  p.sub = w8_sub(p.ht, p.bn, p.cg, K, 1024 + kW8MaxHt * kW8BK + 2 * (E + 1) * (int)sizeof(int));
+  p.sub = w8_sub(p.ht, p.bn, p.cg, K, w8_extra(p.bn, 1, E));
   return p;
 }
 
@@ -1620,6 +1651,7 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
                            const int8_t* wq, const float* sw, void* Y, bool ybf16, bool pdl, cudaStream_t st) {
   if (!offsets && w8_gemv_ok(M, K, N)) return run_w8a8_gemv(xq, -1, sx, M, K, N, wq, sw, Y, ybf16, pdl, st);
   const W8Plan p = offsets ? plan_moe_w8a8(M, K, N, E) : plan_w8a8(M, K, N);
+  if (p.cg == 0) return fail(LBQ_ERR_UNSUPPORTED, "the forced W8A8 plan cannot take M=%d K=%d N=%d", M, K, N);
   W8a8Args a{};
   a.Y = Y;
   a.sx = sx;
@@ -1628,6 +1660,10 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
   a.M = M; a.N = N; a.E = E;
   a.ht = p.ht; a.n_tiles = p.n_tiles;
   a.bn = p.bn; a.m_tiles = p.m_tiles;
+  a.n_unit = w8_unit(N);
+  const int n_units = (N + a.n_unit - 1) / a.n_unit;
+  a.n_each = n_units / p.n_tiles;
+  a.n_more = n_units % p.n_tiles;
   a.sub = p.sub; a.splits = p.splits;
   a.k_whole = K / kW8BK;
   a.k_tail = K % kW8BK != 0;
@@ -1660,8 +1696,7 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
   }
   if (!ok) return fail(LBQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the W8A8 operands");
 
-  // alignment, the slack behind the ring, and the routed form's tile counts
-  const int extra = 1024 + kW8MaxHt * kW8BK + (offsets ? 2 * (E + 1) * (int)sizeof(int) : 0);
+  const int extra = w8_extra(p.bn, p.splits, offsets ? E : 0);
   a.stages = std::min(kW8MaxStages, (kW8SmemBudget - extra) / a.stage_bytes);
   const int smem = a.stages * a.stage_bytes + extra;
   const void* fn = p.cg == 2 ? (const void*)w8a8_gemm_kernel<2> : (const void*)w8a8_gemm_kernel<1>;
@@ -1828,6 +1863,26 @@ void lbq_debug_lut3_batch_off(int on) { g_l3b_off = on ? 1 : 0; }
 // CUDA cores (0: none, every M on the tensor cores; -1: the library's choice).
 // Test hook (not in the public header): 1 = every sort on the clustered kernel (0 = the library's choice).
 void lbq_debug_sort_cluster(int on) { g_sort_work = on ? 0 : kSortBlockWork; }
+// Test hook (not in the public header): the tensor-core plan of the dense W8A8
+// product: blocks per MMA (1 or 2; 0: the library's choice), tiles along N, tokens
+// per tile, blocks sharing K. A plan that the shape cannot take fails the call.
+void lbq_debug_w8a8_plan(int cg, int n_tiles, int bn, int splits) {
+  g_w8_force = W8Plan{};
+  if ((cg == 1 || cg == 2) && n_tiles > 0 && bn > 0 &&
+      (splits == 1 || splits == 2 || splits == 4 || splits == kW8MaxSplits)) {
+    g_w8_force.cg = cg;
+    g_w8_force.n_tiles = n_tiles;
+    g_w8_force.bn = bn;
+    g_w8_force.splits = splits;
+  }
+}
+// Test hook (not in the public header): the plan that the library would choose, as
+// {cg, ht, n_tiles, bn, m_tiles, splits, blocks per stage}.
+void lbq_debug_w8a8_planned(int M, int K, int N, int* out) {
+  const W8Plan p = plan_w8a8(M, K, N);
+  const int v[7] = {p.cg, p.ht, p.n_tiles, p.bn, p.m_tiles, p.splits, p.sub};
+  std::copy(v, v + 7, out);
+}
 void lbq_debug_w8a8_fuse(int m) { g_w8_fuse_max = m; }
 void lbq_debug_w8a8_gemv_max(int m) { g_w8_gemv_max = m < 0 ? kW8GvMaxM : std::min(m, kW8GvMaxM); }
 

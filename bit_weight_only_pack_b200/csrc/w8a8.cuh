@@ -357,8 +357,11 @@ constexpr int kW8BK = 128;        // k per block: one 128-byte swizzle span, fou
 constexpr int kW8MaxHt = 128;     // channels per block and tile (TMEM lanes)
 constexpr int kW8MaxBn = 256;     // tokens per tile (MMA N)
 constexpr int kW8MaxStages = 16;
-constexpr int kW8Threads = 192;   // TMA producer, MMA issuer, four epilogue warps
+constexpr int kW8EpWarps = 8;     // two per TMEM lane quarter
+constexpr int kW8Threads = (2 + kW8EpWarps) * 32;  // TMA producer, MMA issuer, epilogue
 constexpr int kW8MaxSplits = 8;   // blocks that share one tile's K (one cluster)
+constexpr int kW8MaxSplitBn = 128;  // ... of at most so many tokens: their sums lie beside the ring
+static_assert(kW8MaxStages <= 16 && kW8MaxSplits <= 8, "one lane initialises each barrier and flag");
 constexpr int kW8MaxExperts = 2048;
 constexpr int kW8MaxK = 65536;        // 2^16 products of at most 2^14: the sum stays in int32
 constexpr int kW8SmemBudget = 222 * 1024;  // dynamic; barriers and the epilogue's scales take the rest of 227 KB
@@ -370,6 +373,7 @@ struct W8a8Args {
   const int32_t* offsets;   // [E + 1] first row of each expert's run, or null (dense)
   int M, N, E;
   int ht, n_tiles;          // channels per block, tiles along N (CG ht channels each)
+  int n_unit, n_each, n_more;  // dense, CG = 1: a tile has n_unit n_each channels, the first n_more one unit more
   int bn, m_tiles;          // tokens per tile; tiles along M (dense)
   int k_stages, splits;     // ring stages of a tile's K; blocks that share them (CG = 1)
   int sub;                  // whole 128-k blocks per ring stage
@@ -459,15 +463,20 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ int4 ld_cluster4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
@@ -532,8 +541,8 @@ __device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, c
     w.m0 = mt * a.bn;
     w.mh = min(a.bn, a.M - w.m0);
     if (CG == 1) {
-      w.n0 = (int)((long long)nt * a.N / a.n_tiles);
-      w.nh = (int)((long long)(nt + 1) * a.N / a.n_tiles) - w.n0;
+      w.n0 = a.n_unit * (nt * a.n_each + min(nt, a.n_more));
+      w.nh = min(a.N - w.n0, a.n_unit * (a.n_each + (nt < a.n_more ? 1 : 0)));
       return w;
     }
   } else {
@@ -624,36 +633,64 @@ struct W8Ring {
   }
 };
 
-// Columns j .. j + n - 1 (n <= 32) of the block's accumulator into Y: lane =
-// channel, so the warp writes 64 contiguous bytes of every token's row.
 template <bool BF16>
+__device__ __forceinline__ uint32_t w8_round2(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// 32 accumulator columns (tokens; the first n count) of the warp's 32 channels
+// into Y, y at the first token's row and the warp's first channel. PAIR (N even):
+// lanes 2i and 2i + 1 exchange halves, so that a lane holds two channels of one
+// token and a store writes 64 contiguous bytes of two tokens' rows; else one
+// token's per store.
+template <bool BF16, bool PAIR>
 __device__ __forceinline__ void w8_store32(const uint32_t (&v)[32], float sw, const float* sxs, uint16_t* y, int N, int n,
                                            bool row_ok) {
-  uint16_t h[32];
+  const int lane = threadIdx.x & 31;
+  uint32_t h[16];  // tokens 2i (low half), 2i + 1
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 s4 = *reinterpret_cast<const float4*>(sxs + i);
-    h[i] = w8_round<BF16>(((float)(int)v[i] * sw) * s4.x);
-    h[i + 1] = w8_round<BF16>(((float)(int)v[i + 1] * sw) * s4.y);
-    h[i + 2] = w8_round<BF16>(((float)(int)v[i + 2] * sw) * s4.z);
-    h[i + 3] = w8_round<BF16>(((float)(int)v[i + 3] * sw) * s4.w);
+    h[i / 2] = w8_round2<BF16>(((float)(int)v[i] * sw) * s4.x, ((float)(int)v[i + 1] * sw) * s4.y);
+    h[i / 2 + 1] = w8_round2<BF16>(((float)(int)v[i + 2] * sw) * s4.z, ((float)(int)v[i + 3] * sw) * s4.w);
   }
-  if (!row_ok) return;
-  if (n >= 32) {
+  if constexpr (PAIR) {
+    const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) y[(size_t)i * N] = h[i];
+    for (int i = 0; i < 16; ++i) h[i] = __byte_perm(h[i], __shfl_xor_sync(0xFFFFFFFFu, h[i], 1), sel);
+    if (!row_ok) return;
+    const int odd = lane & 1;  // this lane's token of each pair
+    uint32_t* p = reinterpret_cast<uint32_t*>(y + (size_t)odd * N + (lane & ~1));
+    if (n >= 32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[(size_t)i * N] = h[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (2 * i + odd < n) p[(size_t)i * N] = h[i];
+    }
   } else {
+    if (!row_ok) return;
+    y += lane;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) y[(size_t)i * N] = h[i];
+    for (int i = 0; i < 16; ++i) {
+      if (2 * i < n) y[(size_t)(2 * i) * N] = (uint16_t)h[i];
+      if (2 * i + 1 < n) y[(size_t)(2 * i + 1) * N] = (uint16_t)(h[i] >> 16);
+    }
   }
 }
 
 // Warp 0: TMA producer (per ring stage one copy of the tile's weight rows and one
 // of its token rows, `sub` blocks of 128 k each, 128-byte swizzled);
-// warp 1: TMEM owner and MMA issuer; warps 2..5: epilogue, one TMEM lane quarter
-// each (lane = channel). Two accumulators alternate, so the MMAs of a tile run
-// while the last one is written. Persistent: every block (CG = 1) or pair of
+// warp 1: TMEM owner and MMA issuer; warps 2..9: epilogue, two for each TMEM lane
+// quarter (lane = channel), 32 tokens at a time in turn. Two accumulators
+// alternate, so the MMAs of a tile run while the last one is written. Persistent: every block (CG = 1) or pair of
 // blocks (CG = 2) takes every so-manieth tile and the ring runs on across tiles.
 //
 // Warps 0 and 1 run their loops converged and elect a lane for each issue: with
@@ -664,9 +701,9 @@ __device__ __forceinline__ void w8_store32(const uint32_t (&v)[32], float sw, co
 // CG = 1: a tile of fewer than 128 channels loads only its own rows; the MMA's
 // other rows read whatever follows in shared memory (integers, so no NaN can
 // arise) and their lanes are not stored. The ring ends with that much slack.
-// With splits > 1 the blocks of a cluster share the K of one tile: each leaves
-// its int32 sums in its own shared memory, and every block adds all of them for
-// its share of the tokens (integers: in any order the same).
+// With splits > 1 the blocks of a cluster share the K of one tile: each sends its
+// int32 sums to the shared memory of the block that finishes the token (token
+// number modulo splits), which adds them up (integers: in any order the same).
 //
 // CG = 2: two blocks of a cluster share one MMA of 256 channels: each loads its
 // own 128 weight rows and half of the token rows, so the token operand crosses
@@ -677,35 +714,69 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     w8a8_gemm_kernel(const __grid_constant__ W8Maps maps, const W8a8Args a) {
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kW8MaxStages], empty_bar[kW8MaxStages], d_full[2], d_empty[2];
-  __shared__ __align__(16) float sx_sh[4][kW8MaxBn];  // each epilogue warp's copy of its tile's token scales
+  __shared__ __align__(16) float sx_sh[kW8EpWarps][32];  // an epilogue warp's token scales
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int split_ok;
+  __shared__ int split_ok[kW8MaxSplits];  // the block's sums have been sent
   uint8_t* ring = dsmem + ((1024u - (smem_u32(dsmem) & 1023u)) & 1023u);
-  int* start = reinterpret_cast<int*>(ring + (size_t)a.stages * a.stage_bytes + kW8MaxHt * kW8BK);  // routed only
+  uint8_t* behind = ring + (size_t)a.stages * a.stage_bytes + kW8MaxHt * kW8BK;
+  int* start = reinterpret_cast<int*>(behind);  // routed: see w8_expert_tiles
   int* first = start + a.E + 1;
+  int* sums = reinterpret_cast<int*>(behind);   // splits: [token / splits][source block][128 channels]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool split = CG == 1 && a.splits > 1;
   const int rank = (CG == 2 || split) ? (int)cluster_rank() : 0;
   const int share = CG == 2 ? 2 : a.splits;  // blocks per tile
-  w8_griddep_launch_dependents();
-  if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&full_bar[i], 1);
-      mbar_init(&empty_bar[i], 1);
+  const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(full_bar);
+  const uint32_t full_c = CG == 2 ? cluster_addr(full_u, 0) : full_u;  // the barriers that count the bytes
+  const int unit = blockIdx.x / share, units = gridDim.x / share;
+  // this block's stages of each of its tiles
+  const int ks0 = split ? a.k_stages * rank / a.splits : 0;
+  const int ks1 = split ? a.k_stages * (rank + 1) / a.splits : a.k_stages;
+  // weights of k-stage ks of tile w into ring stage `slot`, and the announcement of all the stage's bytes
+  const int tail_stage = a.k_tail ? a.k_stages - 1 : -1;
+  auto load_w = [&](const W8Tile& w, int xrows, int ks, int slot) {
+    const uint32_t st = ring_u + (uint32_t)(slot * a.stage_bytes), bar = full_c + 8u * slot;
+    const bool tail = ks == tail_stage;
+    if (w8_elect()) {
+      if (CG == 1 || rank == 0)
+        mbar_arrive_expect_tx(&full_bar[slot], (uint32_t)(CG * (tail ? 1 : a.sub) * (a.ht + xrows) * kW8BK));
+      if (!tail) w8_load_blocks<CG>(st, &maps.w, w.e * a.N + w.n0, ks * a.sub, bar);
+      else w8_load_tail<CG>(st, &maps.w_tail, w.e * a.N + w.n0, a.k_whole * kW8BK, bar);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4 * CG);
+  };
+  // the weights of the first stages, requested before the kernel that writes the
+  // activations has ended (and, where nothing else is needed for it, before the
+  // rest of the block is set up); returns their number
+  auto load_first = [&](int total) {
+    int pre = 0;
+    for (int tile = unit; tile < total && pre < a.stages; tile += units) {
+      const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
+      const int xrows = w8_x_rows<CG>(a, w8_x_map<CG>(a, w.mh));
+      for (int ks = ks0; ks < ks1 && pre < a.stages; ++ks, ++pre) load_w(w, xrows, ks, pre);
+    }
+    return pre;
+  };
+  const bool early = CG == 1 && a.offsets == nullptr;
+  int pre = 0;
+  w8_griddep_launch_dependents();
+  if (warp == 0) {
+    // a lane per barrier (one lane for all of them takes 1000 clocks)
+    if (lane < a.stages) {
+      mbar_init(&full_bar[lane], 1);
+      mbar_init(&empty_bar[lane], 1);
+    } else if (lane >= kW8MaxStages && lane < kW8MaxStages + 2) {
+      mbar_init(&d_full[lane - kW8MaxStages], 1);
+      mbar_init(&d_empty[lane - kW8MaxStages], kW8EpWarps * CG);
+    } else if (lane >= 24) {
+      split_ok[lane - 24] = 0;
     }
     fence_barrier_init();
-    split_ok = 0;
+    __syncwarp();
+    if (early) pre = load_first(a.m_tiles * a.n_tiles);
   }
   if (warp == 1) w8_tmem_alloc<CG>(&tmem_base_sh, (uint32_t)a.tmem_cols);
-  if (warp == 0 && w8_elect()) {
-    tma_prefetch_desc(&maps.w);
-    tma_prefetch_desc(&maps.x[0]);
-  }
+  if (split) cluster_arrive();  // this block runs and its flags are cleared
   if (a.offsets != nullptr) {
     w8_griddep_wait();  // the offsets come from a kernel before
     w8_expert_tiles(a, start, first);
@@ -713,29 +784,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();  // the other block's barriers are ready
+  if (split) cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const int total = (a.offsets == nullptr ? a.m_tiles : start[a.E]) * a.n_tiles;
-  const int unit = blockIdx.x / share, units = gridDim.x / share;
-  // this block's stages of each of its tiles
-  const int ks0 = split ? a.k_stages * rank / a.splits : 0;
-  const int ks1 = split ? a.k_stages * (rank + 1) / a.splits : a.k_stages;
 
   if (warp == 0) {
-    const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(full_bar);
-    const uint32_t full_c = CG == 2 ? cluster_addr(full_u, 0) : full_u;  // the barriers that count the bytes
-    // weights of k-stage ks of tile w into ring stage `slot`, and the announcement of all the stage's bytes
-    const int tail_stage = a.k_tail ? a.k_stages - 1 : -1;
-    auto load_w = [&](const W8Tile& w, int xrows, int ks, int slot) {
-      const uint32_t st = ring_u + (uint32_t)(slot * a.stage_bytes), bar = full_c + 8u * slot;
-      const bool tail = ks == tail_stage;
-      if (w8_elect()) {
-        if (CG == 1 || rank == 0)
-          mbar_arrive_expect_tx(&full_bar[slot], (uint32_t)(CG * (tail ? 1 : a.sub) * (a.ht + xrows) * kW8BK));
-        if (!tail) w8_load_blocks<CG>(st, &maps.w, w.e * a.N + w.n0, ks * a.sub, bar);
-        else w8_load_tail<CG>(st, &maps.w_tail, w.e * a.N + w.n0, a.k_whole * kW8BK, bar);
-      }
-    };
     auto load_x = [&](int map, int row, int ks, int slot) {
       const uint32_t st = ring_u + (uint32_t)(slot * a.stage_bytes + a.b_off), bar = full_c + 8u * slot;
       if (w8_elect()) {
@@ -743,14 +797,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         else w8_load_tail<CG>(st, &maps.x_tail[map], row, a.k_whole * kW8BK, bar);
       }
     };
-    // the weights of the first stages are requested before the kernel that
-    // writes the activations has ended
-    int pre = 0;
-    for (int tile = unit; tile < total && pre < a.stages; tile += units) {
-      const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
-      const int xrows = w8_x_rows<CG>(a, w8_x_map<CG>(a, w.mh));
-      for (int ks = ks0; ks < ks1 && pre < a.stages; ++ks, ++pre) load_w(w, xrows, ks, pre);
-    }
+    if (!early) pre = load_first(total);
     w8_griddep_wait();
     W8Ring r;
     int it = 0;
@@ -782,7 +829,6 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   } else if (warp == 1) {
     if (CG == 1 || rank == 0) {
       W8Ring r;
-      const uint32_t ring_u = smem_u32(ring);
       int t_iter = 0;
       bool ok = true;
       for (int tile = unit; tile < total && ok; tile += units, ++t_iter) {
@@ -823,82 +869,113 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     }
   } else {
     w8_griddep_wait();  // sx is read (and Y written) after the kernels before
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t d_empty_c = CG == 2 ? cluster_addr(smem_u32(d_empty), 0) : smem_u32(d_empty);
     float* sxs = sx_sh[warp - 2];
+    const int r = 32 * q + lane;  // channel within the block's part of the tile
+    const bool pair = (a.N & 1) == 0;
     int t_iter = 0;
     for (int tile = unit; tile < total; tile += units, ++t_iter) {
       const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
       const int ai = t_iter & 1;
-      const int r = 32 * q + lane;  // channel within the block's part of the tile
       const bool row_ok = r < w.nh;
-      const float sw = row_ok ? *(a.sw + (size_t)w.e * a.N + w.n0 + r) : 0.0f;
-      __syncwarp();  // the last tile's scales have been read
-      for (int j = lane; j < w.mh; j += 32) sxs[j] = *(a.sx + w.m0 + j);
-      __syncwarp();
+      const float sw = row_ok ? a.sw[(size_t)w.e * a.N + w.n0 + r] : 0.0f;
+      const int chunks = (w.mh + 31) >> 5;  // of 32 tokens; this warp takes every second
+      float sxl = 32 * half + lane < w.mh ? a.sx[w.m0 + 32 * half + lane] : 0.0f;
       if (!mbar_wait_sleep(&d_full[ai], (t_iter >> 1) & 1)) break;
       tc_fence_after();
-      if (split) {  // the sums, [token][channel], over the ring: every copy and MMA of this block is done
-        int* part = reinterpret_cast<int*>(ring);
-        for (int j = 0; j < w.mh; j += 32) {
+      if (split) {
+        const uint32_t dst = smem_u32(sums) + 4u * (uint32_t)(rank * kW8MaxHt + r);
+        for (int c = half; c < chunks; c += 2) {
           uint32_t v[32];
-          tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + j), v);
+          tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + 32 * c), v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (j + i < w.mh) part[(j + i) * kW8MaxHt + r] = (int)v[i];
+          for (int i = 0; i < 32; ++i) {
+            const int t = 32 * c + i;
+            if (t < w.mh)
+              st_cluster(cluster_addr(dst + (uint32_t)((t & -a.splits) * kW8MaxHt * 4), (uint32_t)(t & (a.splits - 1))),
+                         (int)v[i]);  // splits: a power of two
+          }
         }
-        if (tid == 64) split_ok = 1;
-        continue;
+        if (warp == 2 && lane < a.splits) st_cluster(cluster_addr(smem_u32(&split_ok[rank]), (uint32_t)lane), 1);
+        break;
       }
-      for (int j = 0; j < w.mh; j += 32) {
+      for (int c = half; c < chunks; c += 2) {
+        __syncwarp();  // the last scales have been read
+        sxs[lane] = sxl;
+        const int j = 32 * c, next = j + 64 + lane;
+        sxl = next < w.mh ? a.sx[w.m0 + next] : 0.0f;
+        __syncwarp();
         uint32_t v[32];
         tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + j), v);
-        if (j + 32 >= w.mh) {  // the accumulator is in registers: the MMAs may fill it again
+        if (c + 2 >= chunks) {  // this warp's part is in registers
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(d_empty_c + 8u * ai);
         }
-        uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + j) * a.N + w.n0 + r;
-        if (a.y_bf16) w8_store32<true>(v, sw, sxs + j, y, a.N, w.mh - j, row_ok);
-        else w8_store32<false>(v, sw, sxs + j, y, a.N, w.mh - j, row_ok);
+        uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + j) * a.N + w.n0 + 32 * q;
+        if (pair) {
+          if (a.y_bf16) w8_store32<true, true>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
+          else w8_store32<false, true>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
+        } else {
+          if (a.y_bf16) w8_store32<true, false>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
+          else w8_store32<false, false>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
+        }
+      }
+      if (chunks <= half) {  // nothing for this warp
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(d_empty_c + 8u * ai);
       }
     }
   }
   __syncwarp();
 
   if (split) {
-    cluster_sync();  // every block's sums are in place
-    if (warp >= 2 && unit < total) {
-      const W8Tile w = w8_tile<CG>(a, start, first, unit, rank);
+    // lane = four channels; warp = every eighth of this block's tokens rank, rank + splits, ...
+    const bool mine = warp >= 2 && unit < total;
+    W8Tile w{};
+    const int c0 = lane << 2;
+    float sw[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sxl = 0.0f;
+    if (mine) {
+      w = w8_tile<CG>(a, start, first, unit, rank);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i < w.nh) sw[i] = a.sw[(size_t)w.e * a.N + w.n0 + c0 + i];
+      const int t = rank + a.splits * (warp - 2 + kW8EpWarps * lane);
+      if (t < w.mh) sxl = a.sx[w.m0 + t];
+    }
+    cluster_sync();  // every block's sums have arrived
+    if (mine) {
       bool ok = true;
-      for (int c = 0; c < a.splits; ++c) ok = ok && ld_cluster(cluster_addr(smem_u32(&split_ok), (uint32_t)c)) != 0;
-      // lane = four channels, warp = a token at a time of every splits-th
-      const int c0 = (lane << 2), left = w.nh - c0;
-      if (ok && left > 0) {
-        float sw[4];
+      for (int c = 0; c < a.splits; ++c) ok = ok && *const_cast<volatile int*>(&split_ok[c]) != 0;
+      const int left = w.nh - c0;
+      for (int i = 0; rank + a.splits * (warp - 2 + kW8EpWarps * i) < w.mh; ++i) {
+        const int k = warp - 2 + kW8EpWarps * i, t = rank + a.splits * k;
+        const float sx = __shfl_sync(0xFFFFFFFFu, sxl, i);
+        int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sw[i] = i < left ? *(a.sw + (size_t)w.e * a.N + w.n0 + c0 + i) : 0.0f;
-        const uint32_t part = smem_u32(ring) + 4u * (uint32_t)c0;
-#pragma unroll 2
-        for (int t = rank + (warp - 2) * a.splits; t < w.mh; t += 4 * a.splits) {
-          int4 sum = make_int4(0, 0, 0, 0);
+        for (int c = 0; c < kW8MaxSplits; ++c)
+          if (c < a.splits) {
+            const int4 v = *reinterpret_cast<const int4*>(sums + (size_t)(k * a.splits + c) * kW8MaxHt + c0);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+          }
+        if (!ok || left <= 0) continue;
+        const float f[4] = {((float)sum.x * sw[0]) * sx, ((float)sum.y * sw[1]) * sx, ((float)sum.z * sw[2]) * sx,
+                            ((float)sum.w * sw[3]) * sx};
+        uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + t) * a.N + w.n0 + c0;
+        if (a.n_unit == 4) {  // rows and tiles in steps of 8 bytes
+          *reinterpret_cast<uint2*>(y) =
+              a.y_bf16 ? make_uint2(w8_round2<true>(f[0], f[1]), w8_round2<true>(f[2], f[3]))
+                       : make_uint2(w8_round2<false>(f[0], f[1]), w8_round2<false>(f[2], f[3]));
+        } else {
 #pragma unroll
-          for (int c = 0; c < kW8MaxSplits; ++c)
-            if (c < a.splits) {
-              const int4 v = ld_cluster4(cluster_addr(part + (uint32_t)(t * kW8MaxHt * 4), (uint32_t)c));
-              sum.x += v.x;
-              sum.y += v.y;
-              sum.z += v.z;
-              sum.w += v.w;
-            }
-          const float sx = *(a.sx + w.m0 + t);
-          const float f[4] = {((float)sum.x * sw[0]) * sx, ((float)sum.y * sw[1]) * sx, ((float)sum.z * sw[2]) * sx,
-                              ((float)sum.w * sw[3]) * sx};
-          uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + t) * a.N + w.n0 + c0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < left) y[i] = a.y_bf16 ? w8_round<true>(f[i]) : w8_round<false>(f[i]);
+          for (int u = 0; u < 4; ++u)
+            if (u < left) y[u] = a.y_bf16 ? w8_round<true>(f[u]) : w8_round<false>(f[u]);
         }
       }
       __syncwarp();
@@ -906,7 +983,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CG == 2 || split) cluster_sync();  // no block's shared memory or barriers are needed any more
+  if (CG == 2) cluster_sync();  // no block's shared memory or barriers are needed any more
   if (warp == 1) {
     tc_fence_after();
     w8_tmem_dealloc<CG>(tmem, (uint32_t)a.tmem_cols);

@@ -1520,6 +1520,7 @@ static W8Plan g_w8_force{};  // test hook: the dense plan's cg, n_tiles, bn and 
 static W8Plan w8_plan_of(int cg, long long n_tiles, int bn, int splits, long long M, int K, int N) {
   const int unit = w8_unit(N);
   W8Plan p{};
+  if (n_tiles < 1 || n_tiles > N || M > (1LL << 31) * bn) return p;
   p.cg = cg;
   p.bn = bn;
   p.splits = splits;
@@ -1532,6 +1533,7 @@ static W8Plan w8_plan_of(int cg, long long n_tiles, int bn, int splits, long lon
 
 // Whether the kernel can run this plan.
 static bool w8_plan_ok(const W8Plan& p, int K, int N) {
+  if (p.cg == 0) return false;
   if (p.ht > kW8MaxHt || p.bn > kW8MaxBn || p.bn % (16 * p.cg) || (long long)p.m_tiles * p.n_tiles > 0x3FFFFFFF) return false;
   if ((long long)p.cg * p.ht * p.n_tiles < N || p.n_tiles < 1) return false;
   if (p.splits == 1) return true;
@@ -1539,7 +1541,7 @@ static bool w8_plan_ok(const W8Plan& p, int K, int N) {
   return p.cg == 1 && p.bn <= kW8MaxSplitBn && tiles <= w8_max_clusters(p.splits) && K / kW8BK >= p.splits * p.sub;
 }
 
-static W8Plan plan_w8a8(long long M, int K, int N) {
+static W8Plan choose_w8a8(long long M, int K, int N) {
   if (g_w8_force.cg) {
     const W8Plan& f = g_w8_force;
     const W8Plan p = w8_plan_of(f.cg, f.n_tiles, f.bn, f.splits, M, K, N);
@@ -1566,7 +1568,7 @@ static W8Plan plan_w8a8(long long M, int K, int N) {
   };
   const long long units = (N + w8_unit(N) - 1) / w8_unit(N), full = (N + kW8MaxHt - 1) / kW8MaxHt;
   const long long m_min = (M + kW8MaxBn - 1) / kW8MaxBn;
-  for (long long mt = m_min; mt <= m_min + m_min / 4 + 4; ++mt) {
+  for (long long mt = m_min; mt <= m_min + std::min<long long>(m_min / 4 + 4, 12); ++mt) {
     const int bn1 = (int)align_up((size_t)((M + mt - 1) / mt), 16), bn2 = (int)align_up((size_t)((M + mt - 1) / mt), 32);
     const long long m_tiles = (M + bn1 - 1) / bn1;
     if (N > kW8MaxHt && M > 64) consider(2, (N + 2 * kW8MaxHt - 1) / (2 * kW8MaxHt), bn2, 1);
@@ -1574,12 +1576,26 @@ static W8Plan plan_w8a8(long long M, int K, int N) {
     const long long w0 = (full * m_tiles + sms - 1) / sms;  // waves of full tiles, filled
     consider(1, std::min(units, std::max(full, w0 * sms / m_tiles)), bn1, 1);
     for (int s = 2; s <= kW8MaxSplits; s *= 2) {
-      const long long nt = w8_max_clusters(s) / m_tiles;
+      const long long nt = w8_max_clusters(s) / m_tiles;  // tiles that leave every cluster one
+      if (nt < full) continue;
       consider(1, full, bn1, s);
       consider(1, std::min(units, nt), bn1, s);
     }
   }
   return best;
+}
+
+// The choice takes a few microseconds, so each thread keeps its last ones.
+static W8Plan plan_w8a8(int M, int K, int N) {
+  struct Entry {
+    int M, K, N;
+    W8Plan plan;
+  };
+  thread_local Entry kept[64] = {};
+  if (g_w8_force.cg) return choose_w8a8(M, K, N);
+  Entry& e = kept[((unsigned)M * 0x9E3779B1u ^ (unsigned)K * 0x85EBCA6Bu ^ (unsigned)N * 0xC2B2AE35u) >> 26];
+  if (e.M != M || e.K != K || e.N != N) e = Entry{M, K, N, choose_w8a8(M, K, N)};
+  return e.plan;
 }
 
 // Routed: the rows of each expert are known on the device only, so the tile is

@@ -107,6 +107,20 @@ def test_helpers_refuse_host_tensors_and_wrong_types(lbq):
             call()
 
 
+def test_every_shape_has_a_plan(lbq):
+    """The dense plan (host code) covers all channels and tokens, in tiles that the kernel takes."""
+    sizes = [1, 2, 3, 7, 8, 9, 15, 16, 17, 64, 100, 128, 129, 255, 256, 257, 500, 1003, 4096, 8192, 28672, 65537, 10 ** 6]
+    for M in sizes + [2 ** 31 - 1]:
+        for N in sizes:
+            for K in (16, 128, 144, 4096, 65536):
+                cg, ht, n_tiles, bn, m_tiles, splits, sub = lbq.lbq_debug_w8a8_planned(M, K, N)
+                if M * N > 2 ** 40:
+                    continue  # more tiles than one launch counts: refused
+                assert cg in (1, 2) and 1 <= ht <= 128 and bn % (16 * cg) == 0 and 16 <= bn <= 256, (M, K, N)
+                assert m_tiles * bn >= M > (m_tiles - 1) * bn and n_tiles * ht * cg >= N, (M, K, N)
+                assert 1 <= sub <= max(1, K // 128) and splits in (1, 2, 4, 8), (M, K, N)
+
+
 # ---------------------------------------------------------------------------- the oracles
 
 def test_oracle_row_quantiser_by_hand():

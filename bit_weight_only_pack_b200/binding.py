@@ -13,6 +13,7 @@ Two layers:
 """
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -299,6 +300,7 @@ def lbq_debug_lut3_batch_off(on):
 def lbq_debug_w8a8_gemv_max(m):
     """Test hook: largest M of the W8A8 product on the CUDA cores (-1 = the library's choice)."""
     _lib.lbq_debug_w8a8_gemv_max(int(m))
+    _w8a8_workspace.cache_clear()
 
 
 def lbq_debug_w8a8_plan(cg, n_tiles=1, bn=16, splits=1):
@@ -734,197 +736,281 @@ def moe_lut3_mx_gemm(codes, scales, top_k, aligned, images, stride, num_local_ex
     return Y
 
 
-def _here():
-    """(current device, its current stream as an integer): read once per call."""
+# The helpers below are called once per kernel in decode loops, so they are written for few Python steps: the common
+# case of each argument check is one inline expression, and _arg is called only to say what is wrong.
+
+_cuda = None        # torch.cuda, torch's dtypes and the current stream's getter, bound at the first call
+_raw_stream = None
+_I8 = _I32 = _F32 = _U8 = _F16 = _BF16 = None
+
+
+def _bind_torch():
+    global _cuda, _raw_stream, _I8, _I32, _F32, _U8, _F16, _BF16
     torch = _torch()
-    dev = torch.cuda.current_device()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 3 us less than building a Stream object
-    return dev, raw(dev) if raw is not None else _stream()
+    _I8, _I32, _F32, _U8 = torch.int8, torch.int32, torch.float32, torch.uint8
+    _F16, _BF16 = torch.float16, torch.bfloat16
+    # the raw stream takes 3 us less than building a Stream object
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _cuda = torch.cuda
 
 
-def _arg(t, name, dtype, shape, dev):
-    """Check a tensor argument: CUDA, on the current device, contiguous, of this dtype and shape."""
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
-        return
+def _arg(t, name, dtype, ndim, shape, dev):
+    """Say what is wrong with a tensor argument that is to be a CUDA tensor on the current device, contiguous, of this
+    dtype and shape (None: any; ndim its dimensions)."""
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}: calls run on the "
                          "current device's stream")
-    if t.dtype is not dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
+    if len(t.shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {list(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
 
 
-def _dims(t, name, n):
-    """The sizes of an n-dimensional CUDA tensor argument."""
+def _device(t, name):
+    """The current device; a host tensor is refused before CUDA is asked for one."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    shape = t.shape
-    if len(shape) != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {list(shape)}")
-    return shape
+    if _cuda is None:
+        _bind_torch()
+    return _cuda.current_device()
 
 
-def _out_arg(t, name, dtype, shape, like, dev):
-    """An output tensor: the given one, checked, or a new one."""
-    if t is None:
-        return like.new_empty(shape, dtype=dtype)
-    _arg(t, name, dtype, shape, dev)
-    return t
+def _half_code(t, name):
+    """The dtype code of an FP16 / BF16 tensor."""
+    dt = t.dtype
+    if dt is _BF16:
+        return 1
+    if dt is _F16:
+        return 0
+    raise TypeError(f"{name} must be FP16 or BF16, got {dt}")
 
 
-def _y_torch_dtype(y_dtype, Y):
-    """The output dtype: the given tensor's, or the named one."""
-    if Y is not None:
-        return Y.dtype
-    torch = _torch()
-    return torch.bfloat16 if y_dtype == "bf16" else torch.float16 if y_dtype == "f16" else y_dtype
+def _new_dtype(y_dtype):
+    return _BF16 if y_dtype == "bf16" else _F16 if y_dtype == "f16" else y_dtype
 
 
 def quantize_int8_rows(X):
     """INT8 activations with one scale per row: X [M, K] FP16/BF16 -> (xq int8 [M, K], sx float32 [M])."""
-    torch = _torch()
-    dt = _dt(X)
-    M, K = _dims(X, "X", 2)
-    dev, stream = _here()
-    _arg(X, "X", X.dtype, (M, K), dev)
-    xq = X.new_empty((M, K), dtype=torch.int8)
-    sx = X.new_empty((M,), dtype=torch.float32)
-    lbq_quantize_int8_rows(X.data_ptr(), dt, M, K, xq.data_ptr(), sx.data_ptr(), stream)
+    dev = _device(X, "X")
+    code = _half_code(X, "X")
+    if not (X.get_device() == dev and X.is_contiguous() and X.dim() == 2):
+        _arg(X, "X", None, 2, None, dev)
+    M, K = X.shape
+    xq = X.new_empty((M, K), dtype=_I8)
+    sx = X.new_empty((M,), dtype=_F32)
+    status = _lib.lbq_quantize_int8_rows(X.data_ptr(), code, M, K, xq.data_ptr(), sx.data_ptr(), _raw_stream(dev))
+    if status:
+        _check(status)
     return xq, sx
 
 
 def quantize_int8_weight(W):
     """INT8 weights with one scale per output channel: W float32 [K, N] -> (wq int8 [N, K], sw float32 [N])."""
-    torch = _torch()
-    K, N = _dims(W, "W", 2)
-    dev, stream = _here()
-    _arg(W, "W", torch.float32, (K, N), dev)
-    wq = W.new_empty((N, K), dtype=torch.int8)
+    dev = _device(W, "W")
+    if not (W.dtype is _F32 and W.get_device() == dev and W.is_contiguous() and W.dim() == 2):
+        _arg(W, "W", _F32, 2, None, dev)
+    K, N = W.shape
+    wq = W.new_empty((N, K), dtype=_I8)
     sw = W.new_empty((N,))
-    lbq_quantize_int8_weight(W.data_ptr(), K, N, wq.data_ptr(), sw.data_ptr(), stream)
+    status = _lib.lbq_quantize_int8_weight(W.data_ptr(), K, N, wq.data_ptr(), sw.data_ptr(), _raw_stream(dev))
+    if status:
+        _check(status)
     return wq, sw
 
 
 def w8a8_gemm(xq, sx, wq, sw, y_dtype="bf16", Y=None):
     """Y[m, n] = sx[m] sw[n] sum_k xq[m, k] wq[n, k] for int8 xq [M, K] and wq [N, K], float32 sx [M] and sw [N]."""
-    torch = _torch()
-    M, K = _dims(xq, "xq", 2)
-    N = _dims(wq, "wq", 2)[0]
-    dev, stream = _here()
-    _arg(xq, "xq", torch.int8, (M, K), dev)
-    _arg(sx, "sx", torch.float32, (M,), dev)
-    _arg(wq, "wq", torch.int8, (N, K), dev)
-    _arg(sw, "sw", torch.float32, (N,), dev)
-    Y = _out_arg(Y, "Y", _y_torch_dtype(y_dtype, Y), (M, N), xq, dev)
-    lbq_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), stream)
+    dev = _device(xq, "xq")
+    if not (xq.dtype is _I8 and xq.get_device() == dev and xq.is_contiguous() and xq.dim() == 2):
+        _arg(xq, "xq", _I8, 2, None, dev)
+    M, K = xq.shape
+    if not (wq.dtype is _I8 and wq.get_device() == dev and wq.is_contiguous() and wq.dim() == 2 and wq.shape[1] == K):
+        _arg(wq, "wq", _I8, 2, (wq.shape[0], K), dev)
+    N = wq.shape[0]
+    if not (sx.dtype is _F32 and sx.get_device() == dev and sx.is_contiguous() and sx.shape == (M,)):
+        _arg(sx, "sx", _F32, 1, (M,), dev)
+    if not (sw.dtype is _F32 and sw.get_device() == dev and sw.is_contiguous() and sw.shape == (N,)):
+        _arg(sw, "sw", _F32, 1, (N,), dev)
+    if Y is None:
+        Y = xq.new_empty((M, N), dtype=_new_dtype(y_dtype))
+    elif not (Y.get_device() == dev and Y.is_contiguous() and Y.shape == (M, N)):
+        _arg(Y, "Y", None, 2, (M, N), dev)
+    status = _lib.lbq_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(),
+                                _half_code(Y, "Y"), _raw_stream(dev))
+    if status:
+        _check(status)
     return Y
+
+
+@functools.lru_cache(maxsize=1024)
+def _w8a8_workspace(M, K):
+    return lbq_w8a8_workspace_size(M, K)
 
 
 def w8a8_linear(X, wq, sw, y_dtype=None, ws=None, Y=None):
     """w8a8_gemm on quantize_int8_rows(X), X [M, K] FP16/BF16, in one call; y_dtype defaults to X's dtype.
-    ws: uint8, lbq_w8a8_workspace_size(M, K) bytes (allocated when not given)."""
-    torch = _torch()
-    dt = _dt(X)
-    M, K = _dims(X, "X", 2)
-    N = _dims(wq, "wq", 2)[0]
-    dev, stream = _here()
-    _arg(X, "X", X.dtype, (M, K), dev)
-    _arg(wq, "wq", torch.int8, (N, K), dev)
-    _arg(sw, "sw", torch.float32, (N,), dev)
-    Y = _out_arg(Y, "Y", X.dtype if y_dtype is None and Y is None else _y_torch_dtype(y_dtype, Y), (M, N), X, dev)
-    if ws is None:
-        ws = X.new_empty((lbq_w8a8_workspace_size(M, K),), dtype=torch.uint8)
-    else:
-        _arg(ws, "ws", torch.uint8, (ws.numel(),), dev)
-    lbq_w8a8_linear(X.data_ptr(), dt, M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(), _dt(Y), ws.data_ptr(),
-                    ws.numel(), stream)
+    ws: uint8, lbq_w8a8_workspace_size(M, K) bytes (allocated when not given; one or two tokens need none)."""
+    dev = _device(X, "X")
+    code = _half_code(X, "X")
+    if not (X.get_device() == dev and X.is_contiguous() and X.dim() == 2):
+        _arg(X, "X", None, 2, None, dev)
+    M, K = X.shape
+    if not (wq.dtype is _I8 and wq.get_device() == dev and wq.is_contiguous() and wq.dim() == 2 and wq.shape[1] == K):
+        _arg(wq, "wq", _I8, 2, (wq.shape[0], K), dev)
+    N = wq.shape[0]
+    if not (sw.dtype is _F32 and sw.get_device() == dev and sw.is_contiguous() and sw.shape == (N,)):
+        _arg(sw, "sw", _F32, 1, (N,), dev)
+    need = _w8a8_workspace(M, K)
+    if ws is not None:
+        if not (ws.dtype is _U8 and ws.get_device() == dev and ws.is_contiguous() and ws.dim() == 1):
+            _arg(ws, "ws", _U8, 1, None, dev)
+    elif need:
+        ws = X.new_empty((need,), dtype=_U8)
+    if Y is None:
+        Y = X.new_empty((M, N)) if y_dtype is None else X.new_empty((M, N), dtype=_new_dtype(y_dtype))
+    elif not (Y.get_device() == dev and Y.is_contiguous() and Y.shape == (M, N)):
+        _arg(Y, "Y", None, 2, (M, N), dev)
+    status = _lib.lbq_w8a8_linear(X.data_ptr(), code, M, K, N, wq.data_ptr(), sw.data_ptr(), Y.data_ptr(),
+                                  _half_code(Y, "Y"), None if ws is None else ws.data_ptr(),
+                                  0 if ws is None else ws.numel(), _raw_stream(dev))
+    if status:
+        _check(status)
     return Y
 
 
 def moe_w8a8_gemm(xq, sx, offsets, wq, sw, y_dtype="bf16", Y=None):
     """The W8A8 product of rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of xq int8 [rows, K] with
     expert e's wq int8 [E, N, K] and sw float32 [E, N]. Rows in no run are not written."""
-    torch = _torch()
-    rows, K = _dims(xq, "xq", 2)
-    E, N, _ = _dims(wq, "wq", 3)
-    dev, stream = _here()
-    _arg(xq, "xq", torch.int8, (rows, K), dev)
-    _arg(sx, "sx", torch.float32, (rows,), dev)
-    _arg(wq, "wq", torch.int8, (E, N, K), dev)
-    _arg(sw, "sw", torch.float32, (E, N), dev)
-    _arg(offsets, "offsets", torch.int32, (E + 1,), dev)
-    Y = _out_arg(Y, "Y", _y_torch_dtype(y_dtype, Y), (rows, N), xq, dev)
-    lbq_moe_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), rows, K, N, offsets.data_ptr(), E, wq.data_ptr(), sw.data_ptr(),
-                      Y.data_ptr(), _dt(Y), stream)
+    dev = _device(xq, "xq")
+    if not (xq.dtype is _I8 and xq.get_device() == dev and xq.is_contiguous() and xq.dim() == 2):
+        _arg(xq, "xq", _I8, 2, None, dev)
+    rows, K = xq.shape
+    if not (wq.dtype is _I8 and wq.get_device() == dev and wq.is_contiguous() and wq.dim() == 3 and wq.shape[2] == K):
+        _arg(wq, "wq", _I8, 3, tuple(wq.shape[:2]) + (K,), dev)
+    E, N, _ = wq.shape
+    if not (sx.dtype is _F32 and sx.get_device() == dev and sx.is_contiguous() and sx.shape == (rows,)):
+        _arg(sx, "sx", _F32, 1, (rows,), dev)
+    if not (sw.dtype is _F32 and sw.get_device() == dev and sw.is_contiguous() and sw.shape == (E, N)):
+        _arg(sw, "sw", _F32, 2, (E, N), dev)
+    if not (offsets.dtype is _I32 and offsets.get_device() == dev and offsets.is_contiguous()
+            and offsets.shape == (E + 1,)):
+        _arg(offsets, "offsets", _I32, 1, (E + 1,), dev)
+    if Y is None:
+        Y = xq.new_empty((rows, N), dtype=_new_dtype(y_dtype))
+    elif not (Y.get_device() == dev and Y.is_contiguous() and Y.shape == (rows, N)):
+        _arg(Y, "Y", None, 2, (rows, N), dev)
+    status = _lib.lbq_moe_w8a8_gemm(xq.data_ptr(), sx.data_ptr(), rows, K, N, offsets.data_ptr(), E, wq.data_ptr(),
+                                    sw.data_ptr(), Y.data_ptr(), _half_code(Y, "Y"), _raw_stream(dev))
+    if status:
+        _check(status)
     return Y
 
 
 def moe_sort(topk_ids, num_experts):
     """topk_ids int32 [T, top_k] -> (row_of_pair int32 [T, top_k], pair_of_row int32 [T * top_k], offsets int32
     [num_experts + 1]): the pairs in ascending (expert, pair) order; -1 for pairs whose id is no expert."""
-    torch = _torch()
-    T, top_k = _dims(topk_ids, "topk_ids", 2)
-    dev, stream = _here()
-    _arg(topk_ids, "topk_ids", torch.int32, (T, top_k), dev)
-    row = topk_ids.new_empty((T, top_k))
-    pair = topk_ids.new_empty((T * top_k,))
+    dev = _device(topk_ids, "topk_ids")
+    if not (topk_ids.dtype is _I32 and topk_ids.get_device() == dev and topk_ids.is_contiguous()
+            and topk_ids.dim() == 2):
+        _arg(topk_ids, "topk_ids", _I32, 2, None, dev)
+    pairs = topk_ids.numel()
+    row = topk_ids.new_empty(topk_ids.shape)
+    pair = topk_ids.new_empty((pairs,))
     offsets = topk_ids.new_empty((max(num_experts, 0) + 1,))
-    lbq_moe_sort(topk_ids.data_ptr(), T * top_k, num_experts, row.data_ptr(), pair.data_ptr(), offsets.data_ptr(),
-                 stream)
+    status = _lib.lbq_moe_sort(topk_ids.data_ptr(), pairs, num_experts, row.data_ptr(), pair.data_ptr(),
+                               offsets.data_ptr(), _raw_stream(dev))
+    if status:
+        _check(status)
     return row, pair, offsets
 
 
 def moe_permute(X, row_of_pair, Xs=None):
     """Xs[row_of_pair[t, j]] = X[t] for X [T, H] of any dtype; Xs [rows, H], by default T * top_k rows. Rows that no
     entry names (there are such when pairs were dropped) are not written."""
-    torch = _torch()
-    T, H = _dims(X, "X", 2)
-    top_k = _dims(row_of_pair, "row_of_pair", 2)[1]
-    dev, stream = _here()
-    _arg(X, "X", X.dtype, (T, H), dev)
-    _arg(row_of_pair, "row_of_pair", torch.int32, (T, top_k), dev)
-    rows = T * top_k if Xs is None else _dims(Xs, "Xs", 2)[0]
-    Xs = _out_arg(Xs, "Xs", X.dtype, (rows, H), X, dev)
-    lbq_moe_permute(X.data_ptr(), H * X.element_size(), T, top_k, row_of_pair.data_ptr(), rows, Xs.data_ptr(), stream)
+    dev = _device(X, "X")
+    if not (X.get_device() == dev and X.is_contiguous() and X.dim() == 2):
+        _arg(X, "X", None, 2, None, dev)
+    T, H = X.shape
+    if not (row_of_pair.dtype is _I32 and row_of_pair.get_device() == dev and row_of_pair.is_contiguous()
+            and row_of_pair.dim() == 2 and row_of_pair.shape[0] == T):
+        _arg(row_of_pair, "row_of_pair", _I32, 2, (T, row_of_pair.shape[-1]), dev)
+    top_k = row_of_pair.shape[1]
+    if Xs is None:
+        rows = T * top_k
+        Xs = X.new_empty((rows, H))
+    else:
+        if not (Xs.dtype is X.dtype and Xs.get_device() == dev and Xs.is_contiguous() and Xs.dim() == 2
+                and Xs.shape[1] == H):
+            _arg(Xs, "Xs", X.dtype, 2, (Xs.shape[0], H), dev)
+        rows = Xs.shape[0]
+    status = _lib.lbq_moe_permute(X.data_ptr(), H * X.element_size(), T, top_k, row_of_pair.data_ptr(), rows,
+                                  Xs.data_ptr(), _raw_stream(dev))
+    if status:
+        _check(status)
     return Xs
 
 
 def moe_combine(Ys, row_of_pair, weights=None, out=None):
     """out[t] = sum_j weights[t, j] Ys[row_of_pair[t, j]] (FP32, rounded once) for Ys [rows, H] FP16/BF16 and float32
     weights [T, top_k] (None: 1); entries of row_of_pair outside the rows add nothing."""
-    torch = _torch()
-    dt = _dt(Ys)
-    rows, H = _dims(Ys, "Ys", 2)
-    T, top_k = _dims(row_of_pair, "row_of_pair", 2)
-    dev, stream = _here()
-    _arg(Ys, "Ys", Ys.dtype, (rows, H), dev)
-    _arg(row_of_pair, "row_of_pair", torch.int32, (T, top_k), dev)
-    if weights is not None:
-        _arg(weights, "weights", torch.float32, (T, top_k), dev)
-    out = _out_arg(out, "out", Ys.dtype, (T, H), Ys, dev)
-    lbq_moe_combine(Ys.data_ptr(), dt, rows, H, row_of_pair.data_ptr(),
-                    weights.data_ptr() if weights is not None else None, T, top_k, out.data_ptr(), stream)
+    dev = _device(Ys, "Ys")
+    code = _half_code(Ys, "Ys")
+    if not (Ys.get_device() == dev and Ys.is_contiguous() and Ys.dim() == 2):
+        _arg(Ys, "Ys", None, 2, None, dev)
+    if not (row_of_pair.dtype is _I32 and row_of_pair.get_device() == dev and row_of_pair.is_contiguous()
+            and row_of_pair.dim() == 2):
+        _arg(row_of_pair, "row_of_pair", _I32, 2, None, dev)
+    rows, H = Ys.shape
+    pairs = row_of_pair.shape
+    T, top_k = pairs
+    if weights is not None and not (weights.dtype is _F32 and weights.get_device() == dev and weights.is_contiguous()
+                                    and weights.shape == pairs):
+        _arg(weights, "weights", _F32, 2, pairs, dev)
+    if out is None:
+        out = Ys.new_empty((T, H))
+    elif not (out.dtype is Ys.dtype and out.get_device() == dev and out.is_contiguous() and out.shape == (T, H)):
+        _arg(out, "out", Ys.dtype, 2, (T, H), dev)
+    status = _lib.lbq_moe_combine(Ys.data_ptr(), code, rows, H, row_of_pair.data_ptr(),
+                                  None if weights is None else weights.data_ptr(), T, top_k, out.data_ptr(),
+                                  _raw_stream(dev))
+    if status:
+        _check(status)
     return out
 
 
 def moe_combine_grad(dout, Ys, row_of_pair, weights, dYs=None):
     """Gradients of moe_combine: (dYs [rows, H], dweights float32 [T, top_k]). Rows of dYs that no entry names are
-    not written."""
-    torch = _torch()
-    dt = _dt(Ys)
-    rows, H = _dims(Ys, "Ys", 2)
-    T, top_k = _dims(row_of_pair, "row_of_pair", 2)
-    dev, stream = _here()
-    _arg(Ys, "Ys", Ys.dtype, (rows, H), dev)
-    _arg(row_of_pair, "row_of_pair", torch.int32, (T, top_k), dev)
-    _arg(dout, "dout", Ys.dtype, (T, H), dev)
-    _arg(weights, "weights", torch.float32, (T, top_k), dev)
-    dYs = _out_arg(dYs, "dYs", Ys.dtype, (rows, H), Ys, dev)
-    dweights = weights.new_empty((T, top_k))
-    lbq_moe_combine_grad(dout.data_ptr(), Ys.data_ptr(), dt, rows, H, row_of_pair.data_ptr(), weights.data_ptr(), T,
-                         top_k, dYs.data_ptr(), dweights.data_ptr(), stream)
+    not written; dYs may be Ys itself."""
+    dev = _device(Ys, "Ys")
+    code = _half_code(Ys, "Ys")
+    if not (Ys.get_device() == dev and Ys.is_contiguous() and Ys.dim() == 2):
+        _arg(Ys, "Ys", None, 2, None, dev)
+    if not (row_of_pair.dtype is _I32 and row_of_pair.get_device() == dev and row_of_pair.is_contiguous()
+            and row_of_pair.dim() == 2):
+        _arg(row_of_pair, "row_of_pair", _I32, 2, None, dev)
+    rows, H = Ys.shape
+    pairs = row_of_pair.shape
+    T, top_k = pairs
+    if not (dout.dtype is Ys.dtype and dout.get_device() == dev and dout.is_contiguous() and dout.shape == (T, H)):
+        _arg(dout, "dout", Ys.dtype, 2, (T, H), dev)
+    if not (weights.dtype is _F32 and weights.get_device() == dev and weights.is_contiguous()
+            and weights.shape == pairs):
+        _arg(weights, "weights", _F32, 2, pairs, dev)
+    if dYs is None:
+        dYs = Ys.new_empty((rows, H))
+    elif not (dYs.dtype is Ys.dtype and dYs.get_device() == dev and dYs.is_contiguous() and dYs.shape == (rows, H)):
+        _arg(dYs, "dYs", Ys.dtype, 2, (rows, H), dev)
+    dweights = weights.new_empty(pairs)
+    status = _lib.lbq_moe_combine_grad(dout.data_ptr(), Ys.data_ptr(), code, rows, H, row_of_pair.data_ptr(),
+                                       weights.data_ptr(), T, top_k, dYs.data_ptr(), dweights.data_ptr(),
+                                       _raw_stream(dev))
+    if status:
+        _check(status)
     return dYs, dweights
 
 

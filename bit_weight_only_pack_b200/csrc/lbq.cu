@@ -1617,7 +1617,6 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
 
 // largest pairs x experts of the block-per-expert sort (test hook: 0, the clustered sort always)
 static long long g_sort_work = kSortBlockWork;
-static int g_w8_fuse_max = 2;
 static int g_w8_gemv_max = kW8GvMaxM;  // test hook: largest M on the CUDA-core product
 
 template <bool QUANT, bool BF16>
@@ -1635,9 +1634,11 @@ static bool w8_gemv_ok(int M, int K, int N) {
   if (M > g_w8_gemv_max || (long long)mb * K > 100 * 1024) return false;
   return M <= 4 || (long long)K * N <= (1LL << 25);
 }
-// ... and whether it quantises them itself (they are kept in registers meanwhile).
-static bool w8_gemv_fused(int M, int K, int N) {
-  return M <= g_w8_fuse_max && w8_gemv_ok(M, K, N) && (long long)M * K <= kW8GvFusedVpt * 8 * kW8GvWarps * 32;
+// ... and whether it quantises them itself, keeping them in registers meanwhile.
+// (One token: 4.8 us against 5.7 at K = N = 4096, 11.4 against 12.3 at N = 14336;
+// two: 5.8 against 6.1. Four: 8.4 against 7.5, the blocks then read too much of X.)
+static bool w8_gemv_fused(int M, int K) {
+  return M <= std::min(2, g_w8_gemv_max) && (long long)M * K <= kW8GvFusedVpt * 8 * kW8GvWarps * 32;
 }
 
 // x_dtype < 0: X holds codes with the scales sx.
@@ -1899,7 +1900,6 @@ void lbq_debug_w8a8_planned(int M, int K, int N, int* out) {
   const int v[7] = {p.cg, p.ht, p.n_tiles, p.bn, p.m_tiles, p.splits, p.sub};
   std::copy(v, v + 7, out);
 }
-void lbq_debug_w8a8_fuse(int m) { g_w8_fuse_max = m; }
 void lbq_debug_w8a8_gemv_max(int m) { g_w8_gemv_max = m < 0 ? kW8GvMaxM : std::min(m, kW8GvMaxM); }
 
 // Test hook (not in the public header): prefill stream-K on (1, the library's
@@ -2469,7 +2469,7 @@ lbq_status lbq_w8a8_workspace_size(int M, int K, size_t* bytes) {
   if (!bytes) return fail(LBQ_ERR_INVALID_ARG, "bytes must be non-null");
   lbq_status st = check_w8a8_shape(M, K, 1);
   if (st != LBQ_OK) return st;
-  *bytes = align_up((size_t)M * K, 256) + align_up((size_t)M * sizeof(float), 256);
+  *bytes = w8_gemv_fused(M, K) ? 0 : align_up((size_t)M * K, 256) + align_up((size_t)M * sizeof(float), 256);
   return LBQ_OK;
 }
 
@@ -2479,7 +2479,7 @@ lbq_status lbq_w8a8_linear(const void* X, int x_dtype, int M, int K, int N, cons
   lbq_status st = check_w8a8_shape(M, K, N);
   if (st != LBQ_OK) return st;
   if ((st = lbq_w8a8_workspace_size(M, K, &need)) != LBQ_OK) return st;
-  if (!X || !ws) return fail(LBQ_ERR_INVALID_ARG, "X and ws must be non-null");
+  if (!X || (need && !ws)) return fail(LBQ_ERR_INVALID_ARG, "X and ws must be non-null");
   if (!aligned16(X) || !aligned16(ws)) return fail(LBQ_ERR_INVALID_ARG, "X and ws must be 16-byte aligned");
   if (x_dtype != LBQ_DTYPE_F16 && x_dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "x_dtype %d", x_dtype);
   if (ws_bytes < need) return fail(LBQ_ERR_INVALID_ARG, "workspace of %zu bytes is too small (need %zu)", ws_bytes, need);
@@ -2487,7 +2487,7 @@ lbq_status lbq_w8a8_linear(const void* X, int x_dtype, int M, int K, int N, cons
   int8_t* xq = static_cast<int8_t*>(ws);
   float* sx = reinterpret_cast<float*>(xq + align_up((size_t)M * K, 256));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (w8_gemv_fused(M, K, N))
+  if (need == 0)  // quantised in the product's blocks
     return run_w8a8_gemv(X, x_dtype, nullptr, M, K, N, wq, sw, Y, y_dtype == LBQ_DTYPE_BF16, g_pdl != 0, s);
   if ((st = run_quantize_rows(X, x_dtype, M, K, xq, sx, s)) != LBQ_OK) return st;
   // the product may start (and fetch weights) while the activations are quantised

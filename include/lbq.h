@@ -558,7 +558,9 @@ lbq_status lbq_w8a8_gemm(const int8_t* xq, const float* sx, int M, int K, int N,
  * product's weight loads under way while the activations are quantised; the
  * weights must not be written by kernels of the same stream that may still run.
  *   ws (device) lbq_w8a8_workspace_size(M, K) bytes, contents free; it holds the
- *      codes and scales, so calls that may run at the same time need one each
+ *      codes and scales, so calls that may run at the same time need one each.
+ *      May be null where the size is 0 (one or two tokens: quantised in the
+ *      product's own blocks)
  * lbq_w8a8_workspace_size writes *bytes (host); no device work. Errors as the
  * two calls, and LBQ_ERR_INVALID_ARG for a workspace that is too small.
  */

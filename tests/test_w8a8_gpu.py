@@ -55,6 +55,47 @@ def guarded(torch, rows, N, dtype):
     return flat[front:front + rows * N].view(rows, N), untouched
 
 
+def test_helpers_refuse_what_does_not_fit(torch, lbq):
+    """Types, shapes, strides and outputs, before anything is launched."""
+    z = lambda shape, t: torch.zeros(shape, dtype=t, device="cuda")  # noqa: E731
+    f16, f32, i8, i32 = torch.float16, torch.float32, torch.int8, torch.int32
+    x, xq, sx, wq, sw = z((4, 64), f16), z((4, 64), i8), z(4, f32), z((8, 64), i8), z(8, f32)
+    rows, w, y = z((4, 2), i32), z((4, 2), f32), z((8, 64), f16)
+    before = lbq.lbq_launch_count()
+    for bad, call in [
+        (TypeError, lambda: lbq.quantize_int8_rows(x.float())),
+        (ValueError, lambda: lbq.quantize_int8_rows(x[0])),
+        (ValueError, lambda: lbq.quantize_int8_rows(z((4, 128), f16)[:, ::2])),
+        (TypeError, lambda: lbq.quantize_int8_weight(x)),
+        (TypeError, lambda: lbq.w8a8_gemm(x, sx, wq, sw)),
+        (TypeError, lambda: lbq.w8a8_gemm(xq, sx.double(), wq, sw)),
+        (ValueError, lambda: lbq.w8a8_gemm(xq, sx[:3], wq, sw)),
+        (ValueError, lambda: lbq.w8a8_gemm(xq, sx, z((8, 48), i8), sw)),
+        (ValueError, lambda: lbq.w8a8_gemm(xq, sx, wq, sw, Y=z((4, 9), f16))),
+        (TypeError, lambda: lbq.w8a8_gemm(xq, sx, wq, sw, Y=z((4, 8), f32))),
+        (TypeError, lambda: lbq.w8a8_linear(x.float(), wq, sw)),
+        (ValueError, lambda: lbq.w8a8_linear(x, wq.t(), sw)),
+        (lbq.LbqError, lambda: lbq.w8a8_linear(x, wq, sw, ws=z(16, torch.uint8))),
+        (lbq.LbqError, lambda: lbq.w8a8_gemm(xq.view(-1)[8:8 + 192].view(3, 64), sx[:3], wq, sw)),  # misaligned
+        (ValueError, lambda: lbq.moe_w8a8_gemm(xq, sx, z(2, i32), z((2, 8, 64), i8), z((2, 8), f32))),
+        (TypeError, lambda: lbq.moe_w8a8_gemm(xq, sx, z(3, torch.int64), z((2, 8, 64), i8), z((2, 8), f32))),
+        (TypeError, lambda: lbq.moe_sort(rows.long(), 4)),
+        (lbq.LbqError, lambda: lbq.moe_sort(rows, 0)),
+        (ValueError, lambda: lbq.moe_permute(x, rows[:3])),
+        (TypeError, lambda: lbq.moe_permute(x, rows, Xs=z((8, 64), torch.bfloat16))),
+        (ValueError, lambda: lbq.moe_permute(x, rows, Xs=z((8, 63), f16))),
+        (TypeError, lambda: lbq.moe_combine(y.float(), rows, w)),
+        (ValueError, lambda: lbq.moe_combine(y, rows, w[:3])),
+        (TypeError, lambda: lbq.moe_combine(y, rows, w.half())),
+        (TypeError, lambda: lbq.moe_combine_grad(x.bfloat16(), y, rows, w)),
+        (ValueError, lambda: lbq.moe_combine_grad(x[:3], y, rows, w)),
+        (ValueError, lambda: lbq.moe_combine_grad(x, y, rows, w, dYs=y[:7])),
+    ]:
+        with pytest.raises(bad):
+            call()
+    assert lbq.lbq_launch_count() == before
+
+
 # ---------------------------------------------------------------------------- quantisers
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -112,17 +153,17 @@ def test_quantize_weight_is_bit_exact(torch, lbq, K, N):
 
 # ---------------------------------------------------------------------------- dense product
 
-@pytest.mark.parametrize("ydt", ["f16", "bf16"])
-@pytest.mark.parametrize("M,K,N", [
+SHAPES = [
     (1, 16, 1), (1, 4096, 1000), (2, 48, 7), (3, 2064, 90), (4, 128, 28), (5, 8208, 40), (8, 144, 129), (8, 14336, 70), (15, 256, 127), (16, 4112, 1003), (17, 2048, 300),
     (31, 512, 64), (33, 1024, 200), (64, 640, 513), (100, 400, 4099), (255, 128, 130), (256, 272, 257), (257, 384, 96),
     (300, 1040, 1003), (513, 256, 2000), (1000, 192, 77), (1025, 64, 3000),
-])
-@pytest.mark.parametrize("tensor", [False, True])
+]
+
+
+@pytest.mark.parametrize("ydt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N,tensor", [(*s, False) for s in SHAPES] + [(*s, True) for s in SHAPES if s[0] <= 8])
 def test_gemm_matches_the_integer_sums(torch, lbq, M, K, N, ydt, tensor):
-    """The library's choice, and every M on the tensor cores."""
-    if tensor and M > 8:
-        pytest.skip("the same kernel")
+    """The library's choice, and small batches on the tensor cores too."""
     lbq.lbq_debug_w8a8_gemv_max(0 if tensor else -1)
     try:
         check_gemm(torch, lbq, M, K, N, ydt)
@@ -141,6 +182,28 @@ def check_gemm(torch, lbq, M, K, N, ydt):
     lbq.device_status()
     check(torch, Y, w8a8.matmul(xq, sx, wq, sw))
     untouched()
+
+
+@pytest.mark.parametrize("plan", [(1, 1, 16, 1), (1, 3, 32, 2), (1, 2, 16, 4), (1, 5, 128, 8), (1, 3, 48, 4), (1, 7, 256, 1),
+                                  (2, 1, 32, 1), (2, 2, 96, 1), (2, 3, 256, 1)])
+@pytest.mark.parametrize("M,K,N", [(5, 4096, 100), (40, 4112, 127), (77, 4224, 254), (130, 4096, 300), (300, 8192, 256)])
+def test_gemm_plans(torch, lbq, M, K, N, plan):
+    """Every form of the tensor-core kernel (pairs, shared K, token tiles that end inside) on shapes that the library
+    would give another. Plans that a shape cannot take are refused."""
+    cg, n_tiles, bn, splits = plan
+    lbq.lbq_debug_w8a8_gemv_max(0)
+    lbq.lbq_debug_w8a8_plan(cg, n_tiles, bn, splits)
+    try:
+        # too few channel tiles, or more tiles than clusters of `splits` blocks fit at once
+        if n_tiles * cg * 128 < N or (splits > 1 and -(-M // bn) * n_tiles * splits > 148):
+            with pytest.raises(lbq.LbqError):
+                check_gemm(torch, lbq, M, K, N, "bf16")
+        else:
+            check_gemm(torch, lbq, M, K, N, "bf16")
+            check_gemm(torch, lbq, M, K, N, "f16")
+    finally:
+        lbq.lbq_debug_w8a8_plan(0)
+        lbq.lbq_debug_w8a8_gemv_max(-1)
 
 
 @pytest.mark.parametrize("M", [1, 6, 20, 300])

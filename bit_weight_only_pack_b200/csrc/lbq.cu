@@ -1616,9 +1616,15 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   W8Plan p{};
   const int mean = (M + E - 1) / E;
   p.cg = mean > 48 && N > kW8MaxHt ? 2 : 1;
-  p.bn = mean <= 4 ? 16 : mean <= 12 ? 32 : mean <= 24 ? 64 : mean <= 48 ? 128 : 256;
-  const int span = p.cg * kW8MaxHt;
-  p.n_tiles = (N + span - 1) / span;
+  p.bn = mean <= 4 ? 16 : mean <= 12 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : 256;
+  p.n_tiles = (N + p.cg * kW8MaxHt - 1) / (p.cg * kW8MaxHt);
+  if (g_w8_force.cg) {
+    p.cg = g_w8_force.cg;
+    p.bn = g_w8_force.bn;
+    p.n_tiles = std::min(N, g_w8_force.n_tiles);
+    const int x = p.bn / p.cg;
+    if (p.bn > kW8MaxBn || x < 16 || (x & (x - 1)) || (long long)p.n_tiles * p.cg * kW8MaxHt < N) return W8Plan{};
+  }
   p.ht = std::min(kW8MaxHt, (int)align_up((size_t)((N + p.cg * p.n_tiles - 1) / (p.cg * p.n_tiles)), 8));
   p.n_tiles = (N + p.cg * p.ht - 1) / (p.cg * p.ht);
   p.splits = 1;

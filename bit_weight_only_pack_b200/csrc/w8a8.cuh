@@ -644,18 +644,18 @@ __device__ __forceinline__ uint32_t w8_round2(float lo, float hi) {
   }
 }
 
-// 32 accumulator columns (tokens; the first n count) of the warp's 32 channels
+// C accumulator columns (tokens; the first n count) of the warp's 32 channels
 // into Y, y at the first token's row and the warp's first channel. PAIR (N even):
 // lanes 2i and 2i + 1 exchange halves, so that a lane holds two channels of one
 // token and a store writes 64 contiguous bytes of two tokens' rows; else one
 // token's per store.
-template <bool BF16, bool PAIR>
-__device__ __forceinline__ void w8_store32(const uint32_t (&v)[32], float sw, const float* sxs, uint16_t* y, int N, int n,
-                                           bool row_ok) {
+template <int C, bool BF16, bool PAIR>
+__device__ __forceinline__ void w8_store(const uint32_t (&v)[C], float sw, const float* sxs, uint16_t* y, int N, int n,
+                                         bool row_ok) {
   const int lane = threadIdx.x & 31;
-  uint32_t h[16];  // tokens 2i (low half), 2i + 1
+  uint32_t h[C / 2];  // tokens 2i (low half), 2i + 1
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < C; i += 4) {
     const float4 s4 = *reinterpret_cast<const float4*>(sxs + i);
     h[i / 2] = w8_round2<BF16>(((float)(int)v[i] * sw) * s4.x, ((float)(int)v[i + 1] * sw) * s4.y);
     h[i / 2 + 1] = w8_round2<BF16>(((float)(int)v[i + 2] * sw) * s4.z, ((float)(int)v[i + 3] * sw) * s4.w);
@@ -663,33 +663,82 @@ __device__ __forceinline__ void w8_store32(const uint32_t (&v)[32], float sw, co
   if constexpr (PAIR) {
     const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) h[i] = __byte_perm(h[i], __shfl_xor_sync(0xFFFFFFFFu, h[i], 1), sel);
+    for (int i = 0; i < C / 2; ++i) h[i] = __byte_perm(h[i], __shfl_xor_sync(0xFFFFFFFFu, h[i], 1), sel);
     if (!row_ok) return;
     const int odd = lane & 1;  // this lane's token of each pair
     uint32_t* p = reinterpret_cast<uint32_t*>(y + (size_t)odd * N + (lane & ~1));
-    if (n >= 32) {
+    if (n >= C) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[(size_t)i * N] = h[i];
+      for (int i = 0; i < C / 2; ++i) p[(size_t)i * N] = h[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < C / 2; ++i)
         if (2 * i + odd < n) p[(size_t)i * N] = h[i];
     }
   } else {
     if (!row_ok) return;
     y += lane;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < C / 2; ++i) {
       if (2 * i < n) y[(size_t)(2 * i) * N] = (uint16_t)h[i];
       if (2 * i + 1 < n) y[(size_t)(2 * i + 1) * N] = (uint16_t)(h[i] >> 16);
     }
   }
 }
 
+__device__ __forceinline__ void w8_tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void w8_tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+  tmem_wait_ld();
+}
+
+// One warp's share of a finished accumulator: columns in chunks of C, every
+// second (from chunk `half`). `taddr` is the accumulator at the warp's lanes, `y`
+// the tile's first row at the warp's first channel, sx its first token's scale,
+// sx_first that of column C half + lane. The barrier at `empty` is told as soon
+// as the last chunk is in registers.
+template <int C>
+__device__ __forceinline__ void w8_epilogue(uint32_t taddr, int half, int mh, float sw, const float* sx, float sx_first,
+                                            float* sxs, uint16_t* y, int N, int y_bf16, bool row_ok, uint32_t empty) {
+  const int lane = threadIdx.x & 31;
+  float sxl = sx_first;
+  for (int j = C * half; j < mh; j += 2 * C) {
+    __syncwarp();  // the last scales have been read
+    if (lane < C) sxs[lane] = sxl;
+    const int next = j + 2 * C + lane;
+    sxl = lane < C && next < mh ? sx[next] : 0.0f;
+    __syncwarp();
+    uint32_t v[C];
+    w8_tmem_ld(taddr + (uint32_t)j, v);
+    if (j + 2 * C >= mh) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(empty);
+    }
+    uint16_t* yj = y + (size_t)j * N;
+    if ((N & 1) == 0) {
+      if (y_bf16) w8_store<C, true, true>(v, sw, sxs, yj, N, mh - j, row_ok);
+      else w8_store<C, false, true>(v, sw, sxs, yj, N, mh - j, row_ok);
+    } else {
+      if (y_bf16) w8_store<C, true, false>(v, sw, sxs, yj, N, mh - j, row_ok);
+      else w8_store<C, false, false>(v, sw, sxs, yj, N, mh - j, row_ok);
+    }
+  }
+  if (C * half >= mh) {  // nothing for this warp
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(empty);
+  }
+}
+
 // Warp 0: TMA producer (per ring stage one copy of the tile's weight rows and one
 // of its token rows, `sub` blocks of 128 k each, 128-byte swizzled);
 // warp 1: TMEM owner and MMA issuer; warps 2..9: epilogue, two for each TMEM lane
-// quarter (lane = channel), 32 tokens at a time in turn. Two accumulators
+// quarter (lane = channel), 16 or 32 tokens at a time in turn. Two accumulators
 // alternate, so the MMAs of a tile run while the last one is written. Persistent: every block (CG = 1) or pair of
 // blocks (CG = 2) takes every so-manieth tile and the ring runs on across tiles.
 //
@@ -874,20 +923,31 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     const uint32_t d_empty_c = CG == 2 ? cluster_addr(smem_u32(d_empty), 0) : smem_u32(d_empty);
     float* sxs = sx_sh[warp - 2];
     const int r = 32 * q + lane;  // channel within the block's part of the tile
-    const bool pair = (a.N & 1) == 0;
+    // what a tile needs from global memory, requested a tile ahead
+    struct Ahead {
+      W8Tile w;
+      float sw, sx;
+    } cur{}, nxt{};
+    auto request = [&](int tile) {
+      Ahead t{};
+      t.w = w8_tile<CG>(a, start, first, tile, rank);
+      if (r < t.w.nh) t.sw = a.sw[(size_t)t.w.e * a.N + t.w.n0 + r];
+      const int c = (t.w.mh > 32 ? 32 : 16), j = c * half + lane;
+      if (lane < c && j < t.w.mh) t.sx = a.sx[t.w.m0 + j];
+      return t;
+    };
+    if (unit < total) nxt = request(unit);
     int t_iter = 0;
     for (int tile = unit; tile < total; tile += units, ++t_iter) {
-      const W8Tile w = w8_tile<CG>(a, start, first, tile, rank);
+      cur = nxt;
+      if (tile + units < total) nxt = request(tile + units);
+      const W8Tile& w = cur.w;
       const int ai = t_iter & 1;
-      const bool row_ok = r < w.nh;
-      const float sw = row_ok ? a.sw[(size_t)w.e * a.N + w.n0 + r] : 0.0f;
-      const int chunks = (w.mh + 31) >> 5;  // of 32 tokens; this warp takes every second
-      float sxl = 32 * half + lane < w.mh ? a.sx[w.m0 + 32 * half + lane] : 0.0f;
       if (!mbar_wait_sleep(&d_full[ai], (t_iter >> 1) & 1)) break;
       tc_fence_after();
       if (split) {
         const uint32_t dst = smem_u32(sums) + 4u * (uint32_t)(rank * kW8MaxHt + r);
-        for (int c = half; c < chunks; c += 2) {
+        for (int c = half; 32 * c < w.mh; c += 2) {
           uint32_t v[32];
           tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + 32 * c), v);
 #pragma unroll
@@ -901,33 +961,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         if (warp == 2 && lane < a.splits) st_cluster(cluster_addr(smem_u32(&split_ok[rank]), (uint32_t)lane), 1);
         break;
       }
-      for (int c = half; c < chunks; c += 2) {
-        __syncwarp();  // the last scales have been read
-        sxs[lane] = sxl;
-        const int j = 32 * c, next = j + 64 + lane;
-        sxl = next < w.mh ? a.sx[w.m0 + next] : 0.0f;
-        __syncwarp();
-        uint32_t v[32];
-        tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + j), v);
-        if (c + 2 >= chunks) {  // this warp's part is in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(d_empty_c + 8u * ai);
-        }
-        uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)(w.m0 + j) * a.N + w.n0 + 32 * q;
-        if (pair) {
-          if (a.y_bf16) w8_store32<true, true>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
-          else w8_store32<false, true>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
-        } else {
-          if (a.y_bf16) w8_store32<true, false>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
-          else w8_store32<false, false>(v, sw, sxs, y, a.N, w.mh - j, row_ok);
-        }
-      }
-      if (chunks <= half) {  // nothing for this warp
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(d_empty_c + 8u * ai);
-      }
+      const uint32_t taddr = lane_base + (uint32_t)(ai * a.acc_stride), empty = d_empty_c + 8u * ai;
+      uint16_t* y = static_cast<uint16_t*>(a.Y) + (size_t)w.m0 * a.N + w.n0 + 32 * q;
+      if (w.mh > 32)
+        w8_epilogue<32>(taddr, half, w.mh, cur.sw, a.sx + w.m0, cur.sx, sxs, y, a.N, a.y_bf16, r < w.nh, empty);
+      else
+        w8_epilogue<16>(taddr, half, w.mh, cur.sw, a.sx + w.m0, cur.sx, sxs, y, a.N, a.y_bf16, r < w.nh, empty);
     }
   }
   __syncwarp();

@@ -1694,6 +1694,9 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
   a.M = M; a.N = N; a.E = E;
   a.ht = p.ht; a.n_tiles = p.n_tiles;
   a.bn = p.bn; a.m_tiles = p.m_tiles;
+  a.by_n = W8Div::by((uint32_t)p.n_tiles);
+  a.by_band = W8Div::by((uint32_t)p.n_tiles * kSkBand);
+  a.by_last = W8Div::by((uint32_t)std::max(1, p.m_tiles % kSkBand));
   a.n_unit = w8_unit(N);
   const int n_units = (N + a.n_unit - 1) / a.n_unit;
   a.n_each = n_units / p.n_tiles;

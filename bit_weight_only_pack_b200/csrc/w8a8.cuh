@@ -366,6 +366,20 @@ constexpr int kW8MaxExperts = 2048;
 constexpr int kW8MaxK = 65536;        // 2^16 products of at most 2^14: the sum stays in int32
 constexpr int kW8SmemBudget = 222 * 1024;  // dynamic; barriers and the epilogue's scales take the rest of 227 KB
 
+// Division of 0 <= a < 2^31 by a fixed b >= 1 through 2^32 / b (one correction
+// suffices: the product is less than 1 too large). A division by a run-time value
+// costs 100 clocks and more, and every role of a block needs two per tile.
+struct W8Div {
+  uint32_t b, m;
+  static W8Div by(uint32_t d) { return W8Div{d, d > 1 ? (uint32_t)((1ull << 32) / d) + 1u : 0u}; }
+  __device__ __forceinline__ int div(int a) const {
+    if (b == 1) return a;
+    uint32_t q = __umulhi((uint32_t)a, m);
+    if (q * b > (uint32_t)a) --q;
+    return (int)q;
+  }
+};
+
 struct W8a8Args {
   void* Y;                  // [M][N]
   const float* sx;          // [M]
@@ -373,6 +387,7 @@ struct W8a8Args {
   const int32_t* offsets;   // [E + 1] first row of each expert's run, or null (dense)
   int M, N, E;
   int ht, n_tiles;          // channels per block, tiles along N (CG ht channels each)
+  W8Div by_n, by_band, by_last;  // n_tiles; tiles of a band of kSkBand token tiles; token tiles of the last band
   int n_unit, n_each, n_more;  // dense, CG = 1: a tile has n_unit n_each channels, the first n_more one unit more
   int bn, m_tiles;          // tokens per tile; tiles along M (dense)
   int k_stages, splits;     // ring stages of a tile's K; blocks that share them (CG = 1)
@@ -479,8 +494,10 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+// Relaxed: what has to precede it are tensor-memory loads, and tcgen05.wait::ld has
+// waited for those; a release would also wait for the output stores under way.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 // mbar_wait_sleep that also orders what other blocks of the cluster did before their arrivals.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -536,7 +553,12 @@ __device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, c
   W8Tile w;
   int nt = t, mt = 0;
   if (a.offsets == nullptr) {
-    if (a.m_tiles > 1) sk_tile_coords(t, a.n_tiles, a.m_tiles, nt, mt);
+    if (a.m_tiles > 1) {  // sk_tile_coords
+      const int band = a.by_band.div(t), at = t - band * (int)a.by_band.b;
+      const int wide = min(kSkBand, a.m_tiles - band * kSkBand);
+      nt = wide == kSkBand ? at / kSkBand : a.by_last.div(at);
+      mt = band * kSkBand + at - nt * wide;
+    }
     w.e = 0;
     w.m0 = mt * a.bn;
     w.mh = min(a.bn, a.M - w.m0);
@@ -546,7 +568,7 @@ __device__ __forceinline__ W8Tile w8_tile(const W8a8Args& a, const int* start, c
       return w;
     }
   } else {
-    mt = t / a.n_tiles;
+    mt = a.by_n.div(t);
     nt = t - mt * a.n_tiles;
     int lo = 0, hi = a.E;  // the last e with start[e] <= mt
     while (hi - lo > 1) {
@@ -868,12 +890,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     // before the block may exit, its last copies have landed and the commits
     // on its barriers have arrived (after a timed-out wait: the copies, which
     // had that wait's time as well)
-    for (int v = max(0, it - a.stages); v < it; ++v) {
-      const int s = v % a.stages;
-      if (!mbar_wait_sleep(&empty_bar[s], (v / a.stages) & 1)) {
-        if (CG == 1) mbar_wait_sleep(&full_bar[s], (v / a.stages) & 1);
+    for (int i = 0; i < a.stages; ++i) {
+      if (!mbar_wait_sleep(&empty_bar[r.s], r.phase ^ 1)) {
+        if (CG == 1) mbar_wait_sleep(&full_bar[r.s], r.phase ^ 1);
         break;
       }
+      r.next(a.stages);
     }
   } else if (warp == 1) {
     if (CG == 1 || rank == 0) {

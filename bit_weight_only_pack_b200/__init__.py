@@ -21,7 +21,7 @@ from .binding import (  # noqa: F401
     lbq_unpack_lut3_canonical, lbq_version, lbq_workspace_size, lbq_quantize_mxfp8, lbq_lut3_mx_gemm,
     affine_gemv, pack_affine, unpack_affine_canonical, lbq_affine_gemv, lbq_affine_packed_size, lbq_pack_affine,
     lbq_unpack_affine_canonical, quantize_int8, w4a8_gemv, lbq_quantize_int8, lbq_w4a8_gemv,
-    w4a8_gemv_grouped, lbq_w4a8_gemv_grouped, lbq_debug_w4a8_tiled, lbq_debug_lut3_stages, lbq_debug_lut3_batch_off, lbq_debug_gemm_stream_k, lbq_debug_gemm_hold, lbq_debug_gemm_schedule, lbq_debug_tile_coords, lbq_debug_w8a8_gemv_max, lbq_debug_w8a8_plan, lbq_debug_w8a8_planned,
+    w4a8_gemv_grouped, lbq_w4a8_gemv_grouped, lbq_debug_w4a8_tiled, lbq_debug_lut3_stages, lbq_debug_lut3_batch_off, lbq_debug_gemm_stream_k, lbq_debug_gemm_hold, lbq_debug_gemm_schedule, lbq_debug_tile_coords, lbq_debug_w8a8_gemv_max, lbq_debug_w8a8_plan, lbq_debug_w8a8_planned, lbq_debug_w8a8_hold,
     lbq_debug_sort_cluster, make_w4a8_items,
     quantize_int8_rows, quantize_int8_weight, w8a8_gemm, w8a8_linear, moe_w8a8_gemm, lbq_quantize_int8_rows,
     lbq_quantize_int8_weight, lbq_w8a8_gemm, lbq_w8a8_linear, lbq_w8a8_workspace_size, lbq_moe_w8a8_gemm,

@@ -102,6 +102,7 @@ _SIGS = {
     "lbq_moe_combine": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp], _c_int),
     "lbq_moe_combine_grad": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "lbq_debug_w8a8_gemv_max": ([_c_int], None),
+    "lbq_debug_w8a8_hold": ([_c_int], None),
     "lbq_debug_w8a8_plan": ([_c_int, _c_int, _c_int, _c_int], None),
     "lbq_debug_w8a8_planned": ([_c_int, _c_int, _c_int, ctypes.POINTER(_c_int)], None),
     "lbq_debug_sort_cluster": ([_c_int], None),
@@ -306,6 +307,11 @@ def lbq_debug_w8a8_gemv_max(m):
 def lbq_debug_w8a8_plan(cg, n_tiles=1, bn=16, splits=1):
     """Test hook: force the dense W8A8 tensor-core plan (cg = 0: the library's choice)."""
     _lib.lbq_debug_w8a8_plan(cg, n_tiles, bn, splits)
+
+
+def lbq_debug_w8a8_hold(on):
+    """Test hook: the tensor-core W8A8 kernel copies no token rows, so its bounded waits run out."""
+    _lib.lbq_debug_w8a8_hold(1 if on else 0)
 
 
 def lbq_debug_w8a8_planned(M, K, N):

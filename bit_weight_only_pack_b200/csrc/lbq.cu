@@ -126,17 +126,18 @@ static lbq_status check_header(const ImageHeader& h, int K, int N, int group, in
 // opt-in maximum, once, so later calls with any smem size launch.
 static int occupancy_for(const void* fn, int block, int smem) {
   static std::mutex mu;
-  static std::map<const void*, bool> raised;
+  static std::map<std::pair<const void*, int>, bool> raised;  // the limit is the function's on one device
   static std::map<std::pair<const void*, long long>, int> cache;
   std::lock_guard<std::mutex> lk(mu);
-  if (!raised[fn]) {
-    int dev = 0, optin = 0;
-    cudaGetDevice(&dev);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!raised[{fn, dev}]) {
+    int optin = 0;
     cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     cudaFuncAttributes fa{};
     cudaFuncGetAttributes(&fa, fn);
     cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - (int)fa.sharedSizeBytes);
-    raised[fn] = true;
+    raised[{fn, dev}] = true;
   }
   auto key = std::make_pair(fn, (long long)smem * 4096 + block);
   auto itc = cache.find(key);
@@ -1634,6 +1635,7 @@ static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
 
 // largest pairs x experts of the block-per-expert sort (test hook: 0, the clustered sort always)
 static long long g_sort_work = kSortBlockWork;
+static int g_w8_hold = 0;  // test hook: see lbq_debug_w8a8_hold
 static int g_w8_gemv_max = kW8GvMaxM;  // test hook: largest M on the CUDA-core product
 
 template <bool QUANT, bool BF16>
@@ -1685,7 +1687,10 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
                            const int8_t* wq, const float* sw, void* Y, bool ybf16, bool pdl, cudaStream_t st) {
   if (!offsets && w8_gemv_ok(M, K, N)) return run_w8a8_gemv(xq, -1, sx, M, K, N, wq, sw, Y, ybf16, pdl, st);
   const W8Plan p = offsets ? plan_moe_w8a8(M, K, N, E) : plan_w8a8(M, K, N);
-  if (p.cg == 0) return fail(LBQ_ERR_UNSUPPORTED, "the forced W8A8 plan cannot take M=%d K=%d N=%d", M, K, N);
+  // (a plan forced by a test, or more tiles than one launch counts)
+  if (p.cg == 0) return fail(LBQ_ERR_UNSUPPORTED, "no W8A8 plan for M=%d K=%d N=%d", M, K, N);
+  if (offsets && ((long long)M / p.bn + E) * p.n_tiles > 0x3FFFFFFFLL)
+    return fail(LBQ_ERR_UNSUPPORTED, "rows=%d N=%d: too many tiles for one launch", M, N);
   W8a8Args a{};
   a.Y = Y;
   a.sx = sx;
@@ -1712,6 +1717,7 @@ static lbq_status run_w8a8(const int8_t* xq, const float* sx, int M, int K, int 
   a.tmem_cols = 64;
   while (a.tmem_cols < 2 * a.acc_stride) a.tmem_cols *= 2;
   a.y_bf16 = ybf16 ? 1 : 0;
+  a.hold = g_w8_hold;
 
   W8Maps maps;
   const uint64_t w_rows = (uint64_t)E * (uint64_t)N, k64 = (uint64_t)K;
@@ -1913,6 +1919,11 @@ void lbq_debug_w8a8_plan(int cg, int n_tiles, int bn, int splits) {
     g_w8_force.splits = splits;
   }
 }
+// Test hook (not in the public header): with 1 the tensor-core W8A8 kernel copies no
+// token rows, so its waits run out (after about a second each); it writes nothing
+// and raises the flag that lbq_device_status() reports.
+void lbq_debug_w8a8_hold(int on) { g_w8_hold = on ? 1 : 0; }
+
 // Test hook (not in the public header): the plan that the library would choose, as
 // {cg, ht, n_tiles, bn, m_tiles, splits, blocks per stage}.
 void lbq_debug_w8a8_planned(int M, int K, int N, int* out) {

@@ -396,6 +396,7 @@ struct W8a8Args {
   int stages, a_sub, b_off, stage_bytes;  // bytes: a weight block, offset of the token blocks, a stage
   int acc_stride, tmem_cols;
   int y_bf16;
+  int hold;                 // test hook: the token rows are never copied, so every wait runs out
 };
 
 constexpr int kW8XMaps = 5;
@@ -601,33 +602,51 @@ __device__ __forceinline__ int w8_x_rows(const W8a8Args& a, int map) {
   return a.offsets == nullptr ? a.bn / CG : 16 << map;
 }
 
-// start[0 .. E] and first[0 .. E] of the routed form, by the whole block
-// (contiguous ranges of experts per thread, a warp scan, then the warps' totals).
-// Offsets outside the rows are clamped to them.
-__device__ __forceinline__ void w8_expert_tiles(const W8a8Args& a, int* start, int* first) {
-  __shared__ int warp_sum[kW8Threads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int e = tid; e <= a.E; e += kW8Threads) first[e] = min(max(*(a.offsets + e), 0), a.M);
-  __syncthreads();
-  const int per = (a.E + kW8Threads - 1) / kW8Threads, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
-  auto tiles_of = [&](int e) { return (max(first[e + 1] - first[e], 0) + a.bn - 1) / a.bn; };
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += tiles_of(e);
-  int incl = mine;
+// Inclusive scan over the block's threads (warp shuffles, then the warps' totals).
+template <typename Op>
+__device__ __forceinline__ int w8_block_scan(int v, Op op) {
+  __shared__ int warp_total[kW8Threads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += v;
+    const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v = op(u, v);
   }
-  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();  // the last scan's totals have been read
+  if (lane == 31) warp_total[warp] = v;
   __syncthreads();
-  int o = incl - mine;
-  for (int w = 0; w < warp; ++w) o += warp_sum[w];
+  for (int w = 0; w < warp; ++w) v = op(warp_total[w], v);
+  return v;
+}
+
+// start[0 .. E] and first[0 .. E] of the routed form, by the whole block, each
+// thread a contiguous range of experts. Offsets are clamped to the rows and taken
+// as not decreasing (a smaller one counts as the largest before it), so runs never
+// overlap and the tiles stay below M / bn + E whatever the array holds.
+__device__ __forceinline__ void w8_expert_tiles(const W8a8Args& a, int* start, int* first) {
+  const int per = (a.E + kW8Threads) / kW8Threads;  // of the E + 1 entries
+  const int e0 = min(a.E + 1, (int)threadIdx.x * per), e1 = min(a.E + 1, e0 + per);
+  int top = 0;
+  for (int e = e0; e < e1; ++e) {
+    top = max(top, min(a.offsets[e], a.M));
+    first[e] = top;
+  }
+  const int highest = w8_block_scan(top, [](int x, int y) { return max(x, y); });
+  int before = __shfl_up_sync(0xFFFFFFFFu, highest, 1);
+  __shared__ int warp_top[kW8Threads / 32];
+  if ((threadIdx.x & 31) == 31) warp_top[threadIdx.x >> 5] = highest;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) before = threadIdx.x ? warp_top[(threadIdx.x >> 5) - 1] : 0;
+  for (int e = e0; e < e1; ++e) first[e] = max(first[e], before);
+  __syncthreads();
+  auto tiles_of = [&](int e) { return e < a.E ? (first[e + 1] - first[e] + a.bn - 1) / a.bn : 0; };
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) mine += tiles_of(e);
+  int o = w8_block_scan(mine, [](int x, int y) { return x + y; }) - mine;
   for (int e = e0; e < e1; ++e) {
     start[e] = o;
     o += tiles_of(e);
   }
-  if (tid == kW8Threads - 1) start[a.E] = o;
   __syncthreads();
 }
 
@@ -863,7 +882,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   if (warp == 0) {
     auto load_x = [&](int map, int row, int ks, int slot) {
       const uint32_t st = ring_u + (uint32_t)(slot * a.stage_bytes + a.b_off), bar = full_c + 8u * slot;
-      if (w8_elect()) {
+      if (w8_elect() && !a.hold) {
         if (ks != tail_stage) w8_load_blocks<CG>(st, &maps.x[map], row, ks * a.sub, bar);
         else w8_load_tail<CG>(st, &maps.x_tail[map], row, a.k_whole * kW8BK, bar);
       }

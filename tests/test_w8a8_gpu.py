@@ -359,6 +359,47 @@ def test_routed_rows_in_no_run_are_left(torch, lbq):
         check(torch, Y, np.where(np.isnan(ref), 7.0, ref))
 
 
+def test_routed_offsets_that_decrease_or_lie_outside(torch, lbq):
+    """Whatever the array holds, rows stay inside and belong to one run: an offset counts as the largest before it."""
+    rng = np.random.default_rng(10)
+    rows, E, K, N = 90, 6, 64, 40
+    xq, wq, sx, sw = codes(rng, (rows, K)), codes(rng, (E, N, K)), scales(rng, rows), scales(rng, (E, N))
+    dxq, dsx, dwq, dsw = cuda(torch, xq, sx, wq, sw)
+    for offsets in ([0, 20, 10, 30, 30, 90, 60], [-5, -2 ** 31, 7, 2 ** 31 - 1, 0, 91, 3], [89, 90, 0, 0, 0, 0, 0]):
+        off = np.array(offsets, dtype=np.int64)
+        Y, untouched = guarded(torch, rows, N, torch.bfloat16)
+        Y.fill_(7.0)
+        lbq.moe_w8a8_gemm(dxq, dsx, cuda(torch, off.astype(np.int32))[0], dwq, dsw, Y=Y)
+        ref = w8a8.routed_matmul(xq, sx, np.maximum.accumulate(np.clip(off, 0, rows)), wq, sw)
+        check(torch, Y, np.where(np.isnan(ref), 7.0, ref))
+        untouched()
+
+
+@pytest.mark.parametrize("plan", [(1, 2, 16, 1), (1, 2, 64, 4), (2, 1, 64, 1)])
+def test_waits_run_out(torch, lbq, plan):
+    """Copies that never come: the waits end, nothing is written, the flag is reported, and the next call is right."""
+    rng = np.random.default_rng(11)
+    M, K, N = 40, 4096, 200
+    xq, wq, sx, sw = codes(rng, (M, K)), codes(rng, (N, K)), scales(rng, M), scales(rng, N)
+    dxq, dsx, dwq, dsw = cuda(torch, xq, sx, wq, sw)
+    Y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    lbq.lbq_debug_w8a8_plan(*plan)
+    try:
+        lbq.lbq_debug_w8a8_hold(True)
+        lbq.w8a8_gemm(dxq, dsx, dwq, dsw, Y=Y)
+        lbq.lbq_debug_w8a8_hold(False)
+        with pytest.raises(lbq.LbqError) as e:
+            lbq.device_status()
+        assert e.value.status == lbq.binding.LBQ_ERR_DEVICE
+        assert bool((Y == 7).all())
+        lbq.w8a8_gemm(dxq, dsx, dwq, dsw, Y=Y)
+        lbq.device_status()
+        check(torch, Y, w8a8.matmul(xq, sx, wq, sw))
+    finally:
+        lbq.lbq_debug_w8a8_hold(False)
+        lbq.lbq_debug_w8a8_plan(0)
+
+
 def test_routed_with_one_expert_is_the_dense_product(torch, lbq):
     g = torch.Generator(device="cuda").manual_seed(5)
     xq = torch.randint(-127, 128, (333, 512), generator=g, device="cuda", dtype=torch.int8)

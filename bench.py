@@ -693,6 +693,44 @@ def _secondary_measurements(torch, lbq, workloads, device, peaks, quick):
                                               "bytes_per_launch": b, "weight_copies": len(images)}
         del images
     del W
+    # W8A8 with the activations' quantisation: decode batches and prefill at the gate/up shape, the widest projection
+    for M, K, N in ((1, 4096, 14336), (16, 4096, 14336), (16, 8192, 28672), (2048, 4096, 14336), (8192, 4096, 14336)):
+        copies = max(3, -(-2 * l2_bytes // (K * N)))
+        weights = []
+        for i in range(copies):
+            W = workloads.weights_device(20 + i, K, N, device)
+            weights.append(lbq.quantize_int8_weight(W))
+            del W
+        X = workloads.activations_device(20, M, K, "bf16", device)
+        Yi = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+        need = lbq.lbq_w8a8_workspace_size(M, K)
+        ws8 = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+        def icall(w, s):
+            lbq.lbq_w8a8_linear(X.data_ptr(), 1, M, K, N, w[0].data_ptr(), w[1].data_ptr(), Yi.data_ptr(), 1,
+                                ws8.data_ptr(), need, s)
+
+        ms = rotating_ms(torch, icall, weights, reps=3)
+        b = K * N + 4 * N
+        out[f"w8a8_linear_m{M}_{K}x{N}"] = {"us": ms * 1e3, "GBps": b / ms / 1e6, "frac_hbm": b / ms / 1e6 / hbm,
+                                           "TOPs": 2.0 * M * K * N / ms / 1e9, "weight_copies": copies}
+        del weights, X, Yi, ws8
+    # the MoE layer's rows around its products: sort, copy, combine and gradients (E=256, top-8, H=2048, BF16)
+    for T in (16, 4096):
+        g = torch.Generator(device=device).manual_seed(40 + T)
+        rep = 1 if T < 100 else 3
+        sets = []
+        for _ in range(rep):
+            top, ids = torch.randn((T, 256), generator=g, device=device).topk(8, dim=1)
+            rX = torch.randn((T, 2048), generator=g, device=device).bfloat16()
+            row, _, _ = lbq.moe_sort(ids.int(), 256)
+            sets.append((ids.int(), torch.softmax(top, 1), rX, row, lbq.moe_permute(rX, row)))
+        for name, fn in (("sort", lambda v: lbq.moe_sort(v[0], 256)), ("permute", lambda v: lbq.moe_permute(v[2], v[3])),
+                         ("combine", lambda v: lbq.moe_combine(v[4], v[3], v[1])),
+                         ("combine_grad", lambda v: lbq.moe_combine_grad(v[2], v[4], v[3], v[1]))):
+            ms = rotating_ms(torch, lambda v, s: fn(v), sets, reps=3)
+            out[f"moe_rows_{name}_t{T}"] = {"us": ms * 1e3}
+        del sets
     return out
 
 

@@ -48,9 +48,9 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_block_kernel(const int3
     if (p + 3 < P) {
       id[v] = ld_nc_v4(ids + p);
     } else {
-      if (p < P) id[v].x = (uint32_t)*(ids + p);
-      if (p + 1 < P) id[v].y = (uint32_t)*(ids + p + 1);
-      if (p + 2 < P) id[v].z = (uint32_t)*(ids + p + 2);
+      if (p < P) id[v].x = (uint32_t)ids[p];
+      if (p + 1 < P) id[v].y = (uint32_t)ids[p + 1];
+      if (p + 2 < P) id[v].z = (uint32_t)ids[p + 2];
     }
   }
   int eq = 0, lt = 0;
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* i
   int* mine = count + warp * E;
 #pragma unroll 4
   for (int p = p0 + lane; p < p1; p += 32) {
-    const uint32_t id = (uint32_t)*(ids + p);
+    const uint32_t id = (uint32_t)ids[p];
     if (id < (uint32_t)E) atomicAdd(&mine[id], 1);
   }
   __syncthreads();
@@ -186,11 +186,11 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* i
 
   // (match.any takes some 70 clocks of the SM per warp; log2 E votes are cheaper)
   const int bits = E > 1 ? 32 - __clz(E - 1) : 0;
-  uint32_t next = p0 + lane < p1 ? (uint32_t)*(ids + p0 + lane) : 0xFFFFFFFFu;
+  uint32_t next = p0 + lane < p1 ? (uint32_t)ids[p0 + lane] : 0xFFFFFFFFu;
   for (int p = p0; p < p1; p += 32) {
     const bool in = p + lane < p1;
     const uint32_t id = next;
-    next = p + 32 + lane < p1 ? (uint32_t)*(ids + p + 32 + lane) : 0xFFFFFFFFu;
+    next = p + 32 + lane < p1 ? (uint32_t)ids[p + 32 + lane] : 0xFFFFFFFFu;
     uint32_t same = __ballot_sync(0xFFFFFFFFu, id < (uint32_t)E);  // lanes with this lane's id, bit by bit
     for (int b = 0; b < bits; ++b) {
       const uint32_t set = __ballot_sync(0xFFFFFFFFu, (id >> b) & 1u);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) moe_permute_kernel(const void* X, int T, 
     for (int u = 0; u < U; ++u)
       if (c0 + u * lanes < per_row) v[u] = x[c0 + u * lanes];
     for (int j = 0; j < top_k; ++j) {
-      const int r = *(rp + j);
+      const int r = rp[j];
       if (r < 0 || r >= rows) continue;
       V* y = static_cast<V*>(Xs) + (size_t)r * per_row + c0;
 #pragma unroll
@@ -293,13 +293,13 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const void* Y, int row
       bool use[J];
 #pragma unroll
       for (int i = 0; i < J; ++i) {
-        const int r = j0 + i < top_k ? *(row_of_pair + t * top_k + j0 + i) : -1;
+        const int r = j0 + i < top_k ? row_of_pair[t * top_k + j0 + i] : -1;
         use[i] = r >= 0 && r < rows;
         const V* y = static_cast<const V*>(Y) + (size_t)(use[i] ? r : 0) * per_row + c0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (use[i] && c0 + u * lanes < per_row) v[i][u] = y[u * lanes];
-        w[i] = use[i] && weights ? *(weights + t * top_k + j0 + i) : 1.0f;
+        w[i] = use[i] && weights ? weights[t * top_k + j0 + i] : 1.0f;
       }
 #pragma unroll
       for (int i = 0; i < J; ++i)
@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* dout,
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = j0 + u;
-      r[u] = j < top_k ? *(row_of_pair + t * top_k + j) : -1;
+      r[u] = j < top_k ? row_of_pair[t * top_k + j] : -1;
       if (r[u] >= rows) r[u] = -1;
-      w[u] = r[u] >= 0 ? *(weights + t * top_k + j) : 0.0f;
+      w[u] = r[u] >= 0 ? weights[t * top_k + j] : 0.0f;
       dot[u] = 0.0f;
     }
     for (int c = tid; c < per_row; c += blockDim.x) {

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
   } else {
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
-      sx[m] = m < a.M ? *(a.sx + m) : 0.0f;
+      sx[m] = m < a.M ? a.sx[m] : 0.0f;
       const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.X) + (size_t)m * a.K);
       for (int c = tid; c < chunks; c += kW8GvWarps * 32)
         reinterpret_cast<uint4*>(xs + (size_t)m * a.K)[c] = m < a.M ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
 #pragma unroll
       for (int r = 0; r < kW8GvRows; ++r) {
         const int n = p * kW8GvRows + r;
-        const float sw = n < a.N ? *(a.sw + n) : 0.0f;
+        const float sw = n < a.N ? a.sw[n] : 0.0f;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
           const int sum = __reduce_add_sync(0xFFFFFFFFu, acc[r][m]);

@@ -81,18 +81,21 @@ def test_sort_with_every_pair_at_one_expert(torch, lbq):
 
 
 @pytest.mark.parametrize("name,H", [("float16", 1), ("bfloat16", 7), ("float16", 1003), ("bfloat16", 2048), ("int8", 48),
-                                    ("int8", 33), ("uint8", 2), ("float32", 1), ("float32", 6), ("float64", 5)])
+                                    ("int8", 33), ("int8", 64), ("int8", 65), ("int8", 79), ("int8", 1001), ("float16", 36),
+                                    ("bfloat16", 4130), ("float32", 19), ("float64", 9), ("uint8", 2), ("float32", 1), ("float32", 6), ("float64", 5)])
 @pytest.mark.parametrize("T,top_k,E,dropped", [(1, 3, 8, 0), (50, 2, 7, 0.4), (333, 8, 64, 0)])
 def test_permute(torch, lbq, T, top_k, E, dropped, name, H):
     rng = np.random.default_rng(H + T)
     ids = routing(rng, T, top_k, E, dropped)
     row, _, _ = moe_rows.sort(ids, E)
     X = torch.from_numpy(rng.integers(-100, 100, size=(T, H))).to(getattr(torch, name))
-    Xs = torch.full((T * top_k, H), 101, dtype=X.dtype, device="cuda")
+    flat = torch.full((64 + T * top_k * H + 64,), 101, dtype=X.dtype, device="cuda")
+    Xs = flat[64:64 + T * top_k * H].view(T * top_k, H)
     got = lbq.moe_permute(X.cuda(), torch.from_numpy(row).cuda(), Xs=Xs)
     assert got is Xs
     ref = moe_rows.permute(X.double().numpy(), row, np.full((T * top_k, H), 101.0))
     assert np.array_equal(f64(got), ref)
+    assert bool((flat[:64] == 101).all()) and bool((flat[64 + T * top_k * H:] == 101).all())
 
 
 def test_rows_past_the_buffers_are_skipped(torch, lbq):
@@ -111,8 +114,19 @@ def test_rows_past_the_buffers_are_skipped(torch, lbq):
     assert dw[1].tolist() == [0, 0] and dw[2, 0].item() == 0
 
 
+def guarded(torch, rows, H, t):
+    """An output between two stretches of sevens, and a check that those are as they were."""
+    flat = torch.full((64 + rows * H + 64,), 7.0, dtype=t, device="cuda")
+
+    def untouched():
+        assert bool((flat[:64] == 7).all()) and bool((flat[64 + rows * H:] == 7).all())
+    return flat[64:64 + rows * H].view(rows, H), untouched
+
+
 CASES = [(1, 1, 1, 1, 0), (1, 8, 256, 2048, 0), (16, 8, 64, 512, 0.2), (333, 2, 8, 1003, 0), (40, 5, 7, 6, 0.5),
-         (9, 13, 4, 100, 0), (64, 4, 16, 4100, 0), (3, 6, 8, 16384, 0), (500, 8, 32, 264, 0.05)]
+         (9, 13, 4, 100, 0), (64, 4, 16, 4100, 0), (3, 6, 8, 16384, 0), (500, 8, 32, 264, 0.05),
+         (7, 3, 5, 31, 0.2), (7, 3, 5, 33, 0.2), (21, 4, 5, 34, 0), (33, 8, 16, 77, 0.3), (50, 5, 9, 1001, 0.1), (4, 2, 3, 2047, 0),
+         (6, 9, 12, 2050, 0)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -124,12 +138,16 @@ def test_combine_and_permute_grad(torch, lbq, T, top_k, E, H, dropped, dt):
     Y = torch.from_numpy(rng.standard_normal((T * top_k, H))).to(t)
     w = rng.random((T, top_k)).astype(np.float32)
     drow = torch.from_numpy(row).cuda()
-    for weights, got in ((w, lbq.moe_combine(Y.cuda(), drow, torch.from_numpy(w).cuda())),
-                         (None, lbq.moe_permute_grad(Y.cuda(), drow))):
+    out, untouched = guarded(torch, T, H, t)
+    dX, untouched2 = guarded(torch, T, H, t)
+    for weights, got in ((w, lbq.moe_combine(Y.cuda(), drow, torch.from_numpy(w).cuda(), out=out)),
+                         (None, lbq.moe_permute_grad(Y.cuda(), drow, dX=dX))):
         ref = moe_rows.combine(f64(Y), row, weights)
         size = moe_rows.combine(np.abs(f64(Y)), row, weights)
         fp32 = top_k * 2.0 ** -24 * size
         near(f64(got), ref, fp32 + rounding(torch, np.abs(ref) + fp32, t))
+    untouched()
+    untouched2()
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -141,12 +159,14 @@ def test_combine_grad(torch, lbq, T, top_k, E, H, dropped, dt):
     Y = torch.from_numpy(rng.standard_normal((T * top_k, H))).to(t)
     dout = torch.from_numpy(rng.standard_normal((T, H))).to(t)
     w = rng.random((T, top_k)).astype(np.float32)
-    dY = torch.full((T * top_k, H), 7.0, dtype=t, device="cuda")
+    dY, untouched = guarded(torch, T * top_k, H, t)
+    dY.fill_(7.0)
     _, dw = lbq.moe_combine_grad(dout.cuda(), Y.cuda(), torch.from_numpy(row).cuda(), torch.from_numpy(w).cuda(), dYs=dY)
     rY, rw = moe_rows.combine_grad(f64(dout), f64(Y), row, w, np.full((T * top_k, H), 7.0))
     near(f64(dY), rY, np.abs(rY) * 2.0 ** -24 + rounding(torch, np.abs(rY) * (1 + 2.0 ** -24), t))
     _, size = moe_rows.combine_grad(np.abs(f64(dout)), np.abs(f64(Y)), row, w, np.zeros((T * top_k, H)))
     near(f64(dw), rw, (H + 16) * 2.0 ** -24 * size)
+    untouched()
 
 
 def test_gradients_against_differences(torch, lbq):
@@ -177,9 +197,10 @@ def test_gradients_against_differences(torch, lbq):
     assert ploss(X2) - ploss(X) == dX[4, 11].item()
 
 
-def test_combine_grad_in_place_and_repeatable(torch, lbq):
+@pytest.mark.parametrize("H", [520, 521, 7])
+def test_combine_grad_in_place_and_repeatable(torch, lbq, H):
     rng = np.random.default_rng(2)
-    T, top_k, E, H = 300, 8, 32, 520
+    T, top_k, E = 300, 8, 32
     row = torch.from_numpy(moe_rows.sort(routing(rng, T, top_k, E), E)[0]).cuda()
     Y = torch.randn((T * top_k, H), device="cuda").bfloat16()
     dout, w = torch.randn((T, H), device="cuda").bfloat16(), torch.rand((T, top_k), device="cuda")

@@ -1829,7 +1829,7 @@ static const void* combine_kernel(int n, int top_k) {
   if (n == 8) return top_k > 4 ? (const void*)moe_combine_kernel<BF16, 8, 8, 1> : (const void*)moe_combine_kernel<BF16, 8, 4, 1>;
   return n == 4   ? (const void*)moe_combine_kernel<BF16, 4, 4, 2>
          : n == 2 ? (const void*)moe_combine_kernel<BF16, 2, 4, 4>
-                  : (const void*)moe_combine_kernel<BF16, 1, 4, 4>;
+                  : (const void*)moe_combine_kernel<BF16, 1, 4, 8>;
 }
 
 }  // namespace lbq
@@ -2579,11 +2579,11 @@ lbq_status lbq_moe_permute(const void* X, int row_bytes, int T, int top_k, const
   const void* fn = b == 16  ? (const void*)moe_permute_kernel<16, 1>
                    : b == 8 ? (const void*)moe_permute_kernel<8, 2>
                    : b == 4 ? (const void*)moe_permute_kernel<4, 4>
-                   : b == 2 ? (const void*)moe_permute_kernel<2, 4>
-                            : (const void*)moe_permute_kernel<1, 4>;
+                   : b == 2 ? (const void*)moe_permute_kernel<2, 8>
+                            : (const void*)moe_permute_kernel<1, 8>;
   int per_row = row_bytes / b, shift = 0;
   unsigned grid = 0;
-  if ((st = rows_grid(T, per_row, b == 16 ? 1 : b == 8 ? 2 : 4, &shift, &grid)) != LBQ_OK) return st;
+  if ((st = rows_grid(T, per_row, b == 16 ? 1 : b == 8 ? 2 : b == 4 ? 4 : 8, &shift, &grid)) != LBQ_OK) return st;
   void* args[] = {(void*)&X, (void*)&T, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair, (void*)&rows,
                   (void*)&Xs, (void*)&shift};
   return launch_kernel_ex(fn, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
@@ -2604,7 +2604,7 @@ lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int
   const void* fn = b ? combine_kernel<true>(n, top_k) : combine_kernel<false>(n, top_k);
   int per_row = H / n, shift = 0;
   unsigned grid = 0;
-  if ((st = rows_grid(T, per_row, n == 8 ? 1 : n == 4 ? 2 : 4, &shift, &grid)) != LBQ_OK) return st;
+  if ((st = rows_grid(T, per_row, n == 8 ? 1 : n == 4 ? 2 : n == 2 ? 4 : 8, &shift, &grid)) != LBQ_OK) return st;
   void* args[] = {(void*)&Ys, (void*)&rows, (void*)&T, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
                   (void*)&weights, (void*)&out, (void*)&shift};
   return launch_kernel_ex(fn, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,

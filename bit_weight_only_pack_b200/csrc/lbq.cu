@@ -2625,12 +2625,13 @@ lbq_status lbq_moe_combine_grad(const void* dout, const void* Ys, int dtype, int
     return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be 16-byte aligned");
   const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
   const bool b = dtype == LBQ_DTYPE_BF16;
-  const void* fn = n == 8   ? (b ? (const void*)moe_combine_grad_kernel<true, 8> : (const void*)moe_combine_grad_kernel<false, 8>)
-                   : n == 4 ? (b ? (const void*)moe_combine_grad_kernel<true, 4> : (const void*)moe_combine_grad_kernel<false, 4>)
-                   : n == 2 ? (b ? (const void*)moe_combine_grad_kernel<true, 2> : (const void*)moe_combine_grad_kernel<false, 2>)
-                            : (b ? (const void*)moe_combine_grad_kernel<true, 1> : (const void*)moe_combine_grad_kernel<false, 1>);
+  const void* fn = n == 8   ? (b ? (const void*)moe_combine_grad_kernel<true, 8, 1> : (const void*)moe_combine_grad_kernel<false, 8, 1>)
+                   : n == 4 ? (b ? (const void*)moe_combine_grad_kernel<true, 4, 2> : (const void*)moe_combine_grad_kernel<false, 4, 2>)
+                   : n == 2 ? (b ? (const void*)moe_combine_grad_kernel<true, 2, 4> : (const void*)moe_combine_grad_kernel<false, 2, 4>)
+                            : (b ? (const void*)moe_combine_grad_kernel<true, 1, 4> : (const void*)moe_combine_grad_kernel<false, 1, 4>);
   int per_row = H / n;
-  const int block = std::min(256, std::max(32, (int)align_up((size_t)per_row, 32)));
+  const int u = n == 8 ? 1 : n == 4 ? 2 : 4;  // pieces per thread and step
+  const int block = std::min(256, std::max(32, (int)align_up((size_t)((per_row + u - 1) / u), 32)));
   void* args[] = {(void*)&dout, (void*)&Ys, (void*)&rows, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
                   (void*)&weights, (void*)&dYs, (void*)&dweights};
   return launch_kernel_ex(fn, dim3((unsigned)T), dim3(block), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,

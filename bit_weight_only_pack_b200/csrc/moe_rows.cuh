@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const void* Y, int row
 // thread keeps its part of the four dot products, which meet in shared memory
 // in a fixed order. dY may be Y (a thread reads a place before it writes it), so
 // neither is declared restrict.
-template <bool BF16, int N>
+template <bool BF16, int N, int U>
 __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* dout, const void* Y, int rows,
                                                                int per_row, int top_k,
                                                                const int32_t* row_of_pair,
@@ -348,25 +348,43 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* dout,
       w[u] = r[u] >= 0 ? weights[t * top_k + j] : 0.0f;
       dot[u] = 0.0f;
     }
-    for (int c = tid; c < per_row; c += blockDim.x) {
-      float g[N];
-      unpack_row<BF16, N>(d[c], g);
-      V y[4];
+    const V* y0[4];
+    V* dy0[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (r[u] >= 0) y[u] = static_cast<const V*>(Y)[(size_t)r[u] * per_row + c];
+    for (int u = 0; u < 4; ++u) {
+      y0[u] = static_cast<const V*>(Y) + (size_t)max(r[u], 0) * per_row;
+      dy0[u] = static_cast<V*>(dY) + (size_t)max(r[u], 0) * per_row;
+    }
+    for (uint32_t c0 = (uint32_t)tid; c0 < (uint32_t)per_row; c0 += blockDim.x * U) {
+      V gv[U], yv[4][U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (r[u] >= 0) {
-          float f[N], o[N];
-          unpack_row<BF16, N>(y[u], f);
+      for (int q = 0; q < U; ++q) {
+        const uint32_t c = c0 + q * blockDim.x;
+        if (c >= (uint32_t)per_row) continue;
+        gv[q] = d[c];
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            dot[u] = fmaf(g[n], f[n], dot[u]);
-            o[n] = w[u] * g[n];
+        for (int u = 0; u < 4; ++u)
+          if (r[u] >= 0) yv[u][q] = y0[u][c];
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const uint32_t c = c0 + q * blockDim.x;
+        if (c >= (uint32_t)per_row) continue;
+        float g[N];
+        unpack_row<BF16, N>(gv[q], g);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (r[u] >= 0) {
+            float f[N], o[N];
+            unpack_row<BF16, N>(yv[u][q], f);
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              dot[u] = fmaf(g[n], f[n], dot[u]);
+              o[n] = w[u] * g[n];
+            }
+            dy0[u][c] = pack_row<BF16, N>(o);
           }
-          static_cast<V*>(dY)[(size_t)r[u] * per_row + c] = pack_row<BF16, N>(o);
-        }
+      }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

@@ -899,6 +899,10 @@ PROFILE_CASES = {
     # grouped MoE GEMM (E=256, top-8, H=2048 -> 2 x I=1024), 256 tokens; N is the gate/up width
     "moe256": (2048, 1024, 0, "moe", "mxfp8", 256, None),
     "affine3": (4096, 14336, 64, "affine3", "f16", 1, None),
+    "w8a8m1": (4096, 14336, 0, "w8a8", "bf16", 1, None),
+    "w8a8m16": (8192, 28672, 0, "w8a8", "bf16", 16, None),
+    "w8a8m2048": (4096, 14336, 0, "w8a8", "bf16", 2048, None),
+    "moerows": (2048, 0, 0, "moerows", "bf16", 4096, None),  # K is the rows' width, M the tokens
 }
 
 
@@ -959,6 +963,33 @@ def run_profile_case(name):
         torch.cuda.synchronize()
         lbq.device_status()
         print(f"profile case {name}: {len(images)} launches of K={K} N={N} W4A8 M={M}", flush=True)
+        return 0
+    if mode == "w8a8":
+        # W8A8 on quantised activations, weight copies larger than L2
+        W = workloads.weights_device(7, K, N, device)
+        wq, sw = lbq.quantize_int8_weight(W)
+        del W
+        copies = [wq] + [wq.clone() for _ in range(max(2, (3 * l2) // wq.numel()))]
+        xq, sx = lbq.quantize_int8_rows(workloads.activations_device(7, M, K, xdt, device))
+        for w in copies:
+            lbq.w8a8_gemm(xq, sx, w, sw)
+        torch.cuda.synchronize()
+        lbq.device_status()
+        print(f"profile case {name}: {len(copies)} launches of K={K} N={N} W8A8 M={M}", flush=True)
+        return 0
+    if mode == "moerows":
+        # a MoE layer's rows: sort, copy, combine and its gradient, three times on different rows
+        E, top_k = MOE_LAYER["experts"], MOE_LAYER["top_k"]
+        g = torch.Generator(device=device).manual_seed(7)
+        for _ in range(3):
+            top, ids = torch.randn((M, E), generator=g, device=device).topk(top_k, dim=1)
+            X = torch.randn((M, K), generator=g, device=device).bfloat16()
+            row, _, _ = lbq.moe_sort(ids.int(), E)
+            Xs = lbq.moe_permute(X, row)
+            w = torch.softmax(top, 1)
+            lbq.moe_combine_grad(lbq.moe_combine(Xs, row, w), Xs, row, w)
+        torch.cuda.synchronize()
+        print(f"profile case {name}: 3 runs of T={M} top_k={top_k} E={E} H={K}", flush=True)
         return 0
     if mode.startswith("affine"):
         # b-bit affine GEMV: weight copies larger than L2

@@ -271,7 +271,7 @@ __device__ __forceinline__ typename RowVec<2 * N>::T pack_row(const float (&f)[N
 // token's top_k rows summed in FP32, j ascending, rounded once, J rows times U
 // pieces in flight per thread. weights null: 1.
 template <bool BF16, int N, int J, int U>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const void* Y, int rows, int T, int per_row,
+__global__ void __launch_bounds__(256, N == 8 ? 4 : 2) moe_combine_kernel(const void* Y, int rows, int T, int per_row,
                                                           int top_k, const int32_t* row_of_pair,
                                                           const float* weights, void* out,
                                                           int shift) {

@@ -836,7 +836,7 @@ def w8a8_gemm(xq, sx, wq, sw, y_dtype="bf16", Y=None):
         _arg(xq, "xq", _I8, 2, None, dev)
     M, K = xq.shape
     if not (wq.dtype is _I8 and wq.get_device() == dev and wq.is_contiguous() and wq.dim() == 2 and wq.shape[1] == K):
-        _arg(wq, "wq", _I8, 2, (wq.shape[0], K), dev)
+        _arg(wq, "wq", _I8, 2, (*wq.shape[:1], K), dev)
     N = wq.shape[0]
     if not (sx.dtype is _F32 and sx.get_device() == dev and sx.is_contiguous() and sx.shape == (M,)):
         _arg(sx, "sx", _F32, 1, (M,), dev)
@@ -867,7 +867,7 @@ def w8a8_linear(X, wq, sw, y_dtype=None, ws=None, Y=None):
         _arg(X, "X", None, 2, None, dev)
     M, K = X.shape
     if not (wq.dtype is _I8 and wq.get_device() == dev and wq.is_contiguous() and wq.dim() == 2 and wq.shape[1] == K):
-        _arg(wq, "wq", _I8, 2, (wq.shape[0], K), dev)
+        _arg(wq, "wq", _I8, 2, (*wq.shape[:1], K), dev)
     N = wq.shape[0]
     if not (sw.dtype is _F32 and sw.get_device() == dev and sw.is_contiguous() and sw.shape == (N,)):
         _arg(sw, "sw", _F32, 1, (N,), dev)
@@ -897,7 +897,7 @@ def moe_w8a8_gemm(xq, sx, offsets, wq, sw, y_dtype="bf16", Y=None):
         _arg(xq, "xq", _I8, 2, None, dev)
     rows, K = xq.shape
     if not (wq.dtype is _I8 and wq.get_device() == dev and wq.is_contiguous() and wq.dim() == 3 and wq.shape[2] == K):
-        _arg(wq, "wq", _I8, 3, tuple(wq.shape[:2]) + (K,), dev)
+        _arg(wq, "wq", _I8, 3, (*wq.shape[:2], K), dev)
     E, N, _ = wq.shape
     if not (sx.dtype is _F32 and sx.get_device() == dev and sx.is_contiguous() and sx.shape == (rows,)):
         _arg(sx, "sx", _F32, 1, (rows,), dev)
@@ -944,7 +944,7 @@ def moe_permute(X, row_of_pair, Xs=None):
     T, H = X.shape
     if not (row_of_pair.dtype is _I32 and row_of_pair.get_device() == dev and row_of_pair.is_contiguous()
             and row_of_pair.dim() == 2 and row_of_pair.shape[0] == T):
-        _arg(row_of_pair, "row_of_pair", _I32, 2, (T, row_of_pair.shape[-1]), dev)
+        _arg(row_of_pair, "row_of_pair", _I32, 2, (T, *row_of_pair.shape[1:]), dev)
     top_k = row_of_pair.shape[1]
     if Xs is None:
         rows = T * top_k
@@ -952,7 +952,7 @@ def moe_permute(X, row_of_pair, Xs=None):
     else:
         if not (Xs.dtype is X.dtype and Xs.get_device() == dev and Xs.is_contiguous() and Xs.dim() == 2
                 and Xs.shape[1] == H):
-            _arg(Xs, "Xs", X.dtype, 2, (Xs.shape[0], H), dev)
+            _arg(Xs, "Xs", X.dtype, 2, (*Xs.shape[:1], H), dev)
         rows = Xs.shape[0]
     status = _lib.lbq_moe_permute(X.data_ptr(), H * X.element_size(), T, top_k, row_of_pair.data_ptr(), rows,
                                   Xs.data_ptr(), _raw_stream(dev))

@@ -1788,6 +1788,8 @@ static lbq_status run_quantize_rows(const void* X, int x_dtype, int M, int K, in
 static lbq_status check_w8a8_shape(int M, int K, int N) {
   if (M <= 0 || K <= 0 || N <= 0) return fail(LBQ_ERR_INVALID_ARG, "M=%d K=%d N=%d must be positive", M, K, N);
   if (K % 16) return fail(LBQ_ERR_INVALID_ARG, "K=%d is not a multiple of 16", K);
+  // (rows and channels are counted in int with a tile's room past the end)
+  if (M > kW8MaxRows || N > kW8MaxRows) return fail(LBQ_ERR_UNSUPPORTED, "M=%d N=%d: more than %d", M, N, kW8MaxRows);
   if (K > kW8MaxK) return fail(LBQ_ERR_UNSUPPORTED, "K=%d > %d", K, kW8MaxK);
   return LBQ_OK;
 }
@@ -2531,7 +2533,7 @@ lbq_status lbq_moe_w8a8_gemm(const int8_t* xq, const float* sx, int rows, int K,
   if (st != LBQ_OK) return st;
   if (num_experts <= 0 || num_experts > kW8MaxExperts)
     return fail(LBQ_ERR_INVALID_ARG, "num_experts=%d not in 1..%d", num_experts, kW8MaxExperts);
-  if ((long long)num_experts * N > 0x7FFFFFFFLL) return fail(LBQ_ERR_INVALID_ARG, "num_experts * N too large");
+  if ((long long)num_experts * N > kW8MaxRows) return fail(LBQ_ERR_INVALID_ARG, "num_experts * N too large");
   if (!xq || !sx || !offsets) return fail(LBQ_ERR_INVALID_ARG, "xq, sx and offsets must be non-null");
   if (!aligned16(xq) || !aligned16(sx) || !aligned16(offsets))
     return fail(LBQ_ERR_INVALID_ARG, "xq, sx and offsets must be 16-byte aligned");

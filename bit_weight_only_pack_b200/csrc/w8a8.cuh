@@ -370,6 +370,7 @@ constexpr int kW8MaxSplitBn = 128;  // ... of at most so many tokens: their sums
 static_assert(kW8MaxStages <= 16 && kW8MaxSplits <= 8, "one lane initialises each barrier and flag");
 constexpr int kW8MaxExperts = 2048;
 constexpr int kW8MaxK = 65536;        // 2^16 products of at most 2^14: the sum stays in int32
+constexpr int kW8MaxRows = 0x7FFFFFFF - 1024;  // of either operand
 constexpr int kW8SmemBudget = 222 * 1024;  // dynamic; barriers and the epilogue's scales take the rest of 227 KB
 
 // Division of 0 <= a < 2^31 by a fixed b >= 1 through 2^32 / b (one correction
@@ -733,14 +734,28 @@ __device__ __forceinline__ void w8_store(const uint32_t (&v)[C], float sw, const
   }
 }
 
-__device__ __forceinline__ void w8_tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+// Accumulator columns of the warp's lanes; one statement with its wait, so that no
+// use of a value can be placed before it.
+__device__ __forceinline__ void w8_tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+               "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                 "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                 "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                 "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr) : "memory");
+}
 __device__ __forceinline__ void w8_tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(taddr));
-  tmem_wait_ld();
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                 "=r"(r[15])
+               : "r"(taddr) : "memory");
 }
 
 // One warp's share of a finished accumulator: columns in chunks of C, every
@@ -783,11 +798,11 @@ __device__ __forceinline__ void w8_epilogue(uint32_t taddr, int half, int mh, fl
 }
 
 // Warp 0: TMA producer (per ring stage one copy of the tile's weight rows and one
-// of its token rows, `sub` blocks of 128 k each, 128-byte swizzled);
-// warp 1: TMEM owner and MMA issuer; warps 2..9: epilogue, two for each TMEM lane
-// quarter (lane = channel), 16 or 32 tokens at a time in turn. Two accumulators
-// alternate, so the MMAs of a tile run while the last one is written. Persistent: every block (CG = 1) or pair of
-// blocks (CG = 2) takes every so-manieth tile and the ring runs on across tiles.
+// of its token rows, `sub` blocks of 128 k each, 128-byte swizzled); warp 1: TMEM
+// owner and MMA issuer; warps 2..9: epilogue, two for each TMEM lane quarter (lane =
+// channel), 16 or 32 tokens at a time in turn. Two accumulators alternate, so the
+// MMAs of a tile run while the last one is written. Persistent: block (or pair) u of
+// U takes the tiles u, u + U, ..., and the ring runs on across them.
 //
 // Warps 0 and 1 run their loops converged and elect a lane for each issue: with
 // warp-uniform control flow the descriptors stay in uniform registers. A loop of
@@ -1001,7 +1016,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         const uint32_t dst = smem_u32(sums) + 4u * (uint32_t)(rank * kW8MaxHt + r);
         for (int c = half; 32 * c < w.mh; c += 2) {
           uint32_t v[32];
-          tmem_ld32(lane_base + (uint32_t)(ai * a.acc_stride + 32 * c), v);
+          w8_tmem_ld(lane_base + (uint32_t)(ai * a.acc_stride + 32 * c), v);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int t = 32 * c + i;

@@ -211,6 +211,32 @@ def test_combine_grad_in_place_and_repeatable(torch, lbq, H):
     assert same is Y and torch.equal(Y, dY) and torch.equal(dw2, dw)
 
 
+@pytest.mark.parametrize("H", [2304, 2305])
+def test_offsets_past_32_bits(torch, lbq, H):
+    """Sorted rows of more than 2^31 elements: copied out, combined and their gradient, on sampled tokens."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    T, top_k, E = 131072, 8, 16
+    ids = torch.randint(0, E, (T, top_k), generator=g, device="cuda", dtype=torch.int32)
+    X = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+    row, pair, offsets = lbq.moe_sort(ids, E)
+    Xs = lbq.moe_permute(X, row)
+    assert Xs.numel() > 2 ** 31
+    at = torch.tensor([0, 1, 2 ** 31 // H - 1, 2 ** 31 // H, 2 ** 31 // H + 1, T * top_k - 1], device="cuda")
+    assert torch.equal(Xs[at], X[pair[at].long() // top_k])
+    w = torch.rand((T, top_k), generator=g, device="cuda")
+    out = lbq.moe_combine(Xs, row, w)
+    ts = [0, T // 3, T - 1] + [int(t) for t in (pair[at].long() // top_k)]
+    # every copy of a token's row is the row itself: the combine is the row times the sum of its weights
+    want = X[ts].double() * w[ts].double().sum(1, keepdim=True)
+    size = X[ts].double().abs() * w[ts].double().abs().sum(1, keepdim=True)
+    near(f64(out[ts]), f64(want), f64(size) * (top_k + 1) * 2.0 ** -24 + rounding(torch, f64(size), torch.bfloat16))
+    dY, dw = lbq.moe_combine_grad(X, Xs, row, w, dYs=Xs)
+    ref = X[pair[at].long() // top_k].double() * w.view(-1)[pair[at].long(), None].double()
+    near(f64(dY[at]), f64(ref), np.abs(f64(ref)) * 2.0 ** -24 + rounding(torch, f64(ref) * (1 + 2.0 ** -24), torch.bfloat16))
+    sq = X[ts].double().square().sum(1, keepdim=True).expand(-1, top_k)
+    near(f64(dw[ts]), f64(sq), f64(sq) * (H + 16) * 2.0 ** -24)
+
+
 def test_nan_and_infinity_stay_in_their_rows(torch, lbq):
     row = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
     Y = torch.ones((4, 16), dtype=torch.bfloat16, device="cuda")

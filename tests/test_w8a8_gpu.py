@@ -113,6 +113,16 @@ def test_quantize_rows_is_bit_exact(torch, lbq, M, K, dt):
     assert np.array_equal(xq.cpu().numpy(), rq)
 
 
+def test_quantize_rows_of_the_smallest_and_largest_values(torch, lbq):
+    """Scales whose reciprocal overflows (BF16 subnormals) and the largest finite values, bit for bit."""
+    rng = np.random.default_rng(6)
+    for top in (2.0 ** -133, 2.0 ** -130, 2.0 ** -126, 2.0 ** -120, 3.3e38):
+        X = torch.from_numpy((rng.uniform(-1, 1, size=(6, 128)) * top).astype(np.float32)).bfloat16()
+        xq, sx = lbq.quantize_int8_rows(X.cuda())
+        rq, rs = w8a8.quantize_rows(X.float().numpy())
+        assert np.array_equal(sx.cpu().numpy(), rs) and np.array_equal(xq.cpu().numpy(), rq), top
+
+
 def test_quantize_rows_ties_go_to_even(torch, lbq):
     """amax 127 makes the scale exactly 1: every half-integer is a tie."""
     x = torch.arange(-127, 128).float() / 2  # -63.5 .. 63.5 in halves
@@ -234,6 +244,28 @@ def test_gemm_full_size_sampled(torch, lbq, M, K, N):
     ref = w8a8.matmul(xq[rows].cpu().numpy(), sx[rows].cpu().numpy(), wq[cols].cpu().numpy(), sw[cols].cpu().numpy())
     check(torch, y[rows][:, cols], ref)
     assert torch.equal(y, lbq.w8a8_gemm(xq, sx, wq, sw))
+
+
+def test_offsets_past_32_bits(torch, lbq):
+    """Outputs of more than 2^31 elements and experts' weights of more than 2^32 bytes."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    M, K, N = 140000, 16, 16384
+    xq = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    sx, sw = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    y = lbq.w8a8_gemm(xq, sx, wq, sw)
+    rows = torch.tensor([0, 1, 131071, 131072, 135000, M - 1], device="cuda")
+    n = lambda t: t.cpu().numpy()  # noqa: E731
+    check(torch, y[rows], w8a8.matmul(n(xq[rows]), n(sx[rows]), n(wq), n(sw)))
+    del y, xq, wq
+    E, K, N = 66, 8192, 8192
+    wq = torch.randint(-127, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.rand((E, N), generator=g, device="cuda")
+    xq = torch.randint(-127, 128, (E, K), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(E, generator=g, device="cuda")
+    y = lbq.moe_w8a8_gemm(xq, sx, torch.arange(E + 1, dtype=torch.int32, device="cuda"), wq, sw)
+    for e in (0, 31, 32, 63, 64, E - 1):
+        check(torch, y[e:e + 1], w8a8.matmul(n(xq[e:e + 1]), n(sx[e:e + 1]), n(wq[e]), n(sw[e])))
 
 
 def test_rows_do_not_depend_on_the_batch(torch, lbq):

@@ -540,23 +540,25 @@ lbq_status lbq_quantize_int8_rows(const void* X, int x_dtype, int M, int K, int8
 lbq_status lbq_quantize_int8_weight(const float* W, int K, int N, int8_t* wq, float* sw, void* stream);
 
 /*
- * The W8A8 product, any M >= 1, on tcgen05.mma.kind::i8. The int32 sum is
+ * The W8A8 product, any M >= 1, on tcgen05.mma.kind::i8 (a few tokens: on the
+ * CUDA cores). The int32 sum is
  * converted to FP32 (rounded above 2^24), multiplied by sw[n], then by sx[m],
  * and rounded to nearest in y_dtype; results do not depend on M or the tiling.
  *   xq, sx (device) from lbq_quantize_int8_rows (or any codes and scales)
  *   wq, sw (device) int8 [N, K] codes, float32 [N] scales
  *   Y      (device) [M, N] row-major, y_dtype, fully overwritten
  * No workspace. Errors: LBQ_ERR_INVALID_ARG for null or misaligned pointers or
- * bad sizes, LBQ_ERR_UNSUPPORTED for K > 65536 or an unknown y_dtype, before
- * any launch. Asynchronous on `stream`.
+ * bad sizes, LBQ_ERR_UNSUPPORTED for K > 65536, M or N > 2^31 - 1025 or an unknown
+ * y_dtype, before any launch. Asynchronous on `stream`.
  */
 lbq_status lbq_w8a8_gemm(const int8_t* xq, const float* sx, int M, int K, int N, const int8_t* wq, const float* sw,
                          void* Y, int y_dtype, void* stream);
 
 /*
  * lbq_quantize_int8_rows followed by lbq_w8a8_gemm (the same results), with the
- * product's weight loads under way while the activations are quantised; the
- * weights must not be written by kernels of the same stream that may still run.
+ * product's weight loads under way while the activations are quantised. That
+ * starts after the kernels before on `stream` have ended, unless LBQ_OPT_PDL is
+ * set: then they must not write the weights, as for the GEMV kernels.
  *   ws (device) lbq_w8a8_workspace_size(M, K) bytes, contents free; it holds the
  *      codes and scales, so calls that may run at the same time need one each.
  *      May be null where the size is 0 (one or two tokens: quantised in the
@@ -577,7 +579,8 @@ lbq_status lbq_w8a8_linear(const void* X, int x_dtype, int M, int K, int N, cons
  *           the device, values outside 0 .. rows are clamped to it
  *   wq, sw  (device) int8 [num_experts, N, K], float32 [num_experts, N]
  *   Y       (device) [rows, N] row-major, y_dtype; rows in no expert's run are not written
- * num_experts <= 2048. Errors as lbq_w8a8_gemm. Asynchronous on `stream`.
+ * num_experts <= 2048, num_experts * N <= 2^31 - 1025. Errors as lbq_w8a8_gemm.
+ * Asynchronous on `stream`.
  */
 lbq_status lbq_moe_w8a8_gemm(const int8_t* xq, const float* sx, int rows, int K, int N, const int32_t* offsets,
                              int num_experts, const int8_t* wq, const float* sw, void* Y, int y_dtype, void* stream);

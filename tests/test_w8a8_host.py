@@ -71,6 +71,7 @@ BAD = [  # (call, arguments, status): 1 = invalid argument, 2 = unsupported
     (linear, {"ws_bytes": 4 * 64}, 1),
     (routed, {"E": 2049}, 1), (sort, {"E": 2049}, 1), (sort, {"pairs": 1 << 30}, 1),
     (routed, {"E": 2048, "N": 1 << 21}, 1),
+    *[(f, {k: 2 ** 31 - 1024}, 2) for f, k in ((gemm, "M"), (gemm, "N"), (linear, "N"), (routed, "rows"), (routed, "N"))],
     *[(f, {"T": 1 << 20, "top_k": 1 << 10}, 1) for f in (permute, combine, grad)],
 ]
 

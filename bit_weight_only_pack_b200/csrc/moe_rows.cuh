@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_block_kernel(const int3
     const int p = p0 + v * 128;
     id[v] = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
     if (p + 3 < P) {
-      id[v] = ld_nc_v4(ids + p);
+      id[v] = ld_v4(ids + p);
     } else {
       if (p < P) id[v].x = (uint32_t)ids[p];
       if (p + 1 < P) id[v].y = (uint32_t)ids[p + 1];

@@ -12,9 +12,11 @@
 //    a padded one and the weights, the large operand of a decode step, are
 //    streamed once whatever the batch.
 //
-// What a kernel reads after its griddepcontrol.wait is read by plain loads from
-// pointers without __restrict__ (or by volatile asm): the compiler may move a
-// __ldg, or a load it takes for one, up across the wait.
+// What a kernel before may write is read after griddepcontrol.wait and by coherent
+// loads (ld_v4, ld_once_v4, or plain ones from pointers without __restrict__): the
+// non-coherent path may return what lay there before, and the compiler may move a
+// __ldg, or a load it takes for one, up across the wait. Only weights are read
+// through the non-coherent path.
 #pragma once
 
 #include "common.cuh"
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(256) quantize_int8_rows_warp_kernel(const uint
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = lane + i * 32;
-    v[i] = c < chunks ? ld_stream_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+    v[i] = c < chunks ? ld_once_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) m2 = w8_max_bits(m2, v[i]);
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * blockDim.x;
-    v[i] = c < chunks ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+    v[i] = c < chunks ? ld_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) m2 = w8_max_bits(m2, v[i]);
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
 #pragma unroll
       for (int i = 0; i < kVpt; ++i) {
         const int c = tid + i * (kW8GvWarps * 32);
-        v[m][i] = m < a.M && c < xchunks ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+        v[m][i] = m < a.M && c < xchunks ? ld_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
 #pragma unroll
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
       sx[m] = m < a.M ? a.sx[m] : 0.0f;
       const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.X) + (size_t)m * a.K);
       for (int c = tid; c < chunks; c += kW8GvWarps * 32)
-        reinterpret_cast<uint4*>(xs + (size_t)m * a.K)[c] = m < a.M ? ld_nc_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+        reinterpret_cast<uint4*>(xs + (size_t)m * a.K)[c] = m < a.M ? ld_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
   __syncthreads();

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kAgMaxWarps * 32) affine_gemv_kernel(const Aff
       const uint4* xp = reinterpret_cast<const uint4*>(a.X + (size_t)m * a.K + (size_t)c * 32);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 v = __ldg(xp + i);
+        const uint4 v = ld_v4(xp + i);
         x[m][4 * i] = v.x; x[m][4 * i + 1] = v.y; x[m][4 * i + 2] = v.z; x[m][4 * i + 3] = v.w;
       }
 #pragma unroll

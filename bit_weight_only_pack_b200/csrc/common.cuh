@@ -175,7 +175,10 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
 // 16-byte coherent loads, for what an earlier kernel may write while this one is
 // already resident (a launch that overlaps it reads after griddepcontrol.wait):
 // the non-coherent path is for data that nobody writes during the kernel, and a
-// volatile statement keeps its place behind the wait. ld_once_v4 leaves L1 alone.
+// volatile statement keeps its place behind the wait. Through L1 (ld_v4) they cost
+// the GEMVs nothing (the decode step 3880 GB/s; 3700 past L1, where the two loads
+// of a lane's sector are two fetches); ld_once_v4, which leaves L1 alone, is for
+// rows read once.
 __device__ __forceinline__ uint4 ld_v4(const void* p) {
   uint4 r;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"

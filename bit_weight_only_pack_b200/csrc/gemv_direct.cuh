@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kGdMaxWarps * 32, 1) gemv_direct_kernel(const 
       const uint4* xp = reinterpret_cast<const uint4*>(X + (size_t)c * 32);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const uint4 u = ld_nc_v4(xp + v);
+        const uint4 u = ld_v4(xp + v);
         xr[4 * v + 0] = u.x; xr[4 * v + 1] = u.y; xr[4 * v + 2] = u.z; xr[4 * v + 3] = u.w;
       }
 #pragma unroll
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kGdMaxWarps * 32) gemv_direct_async_kernel(con
         load_xq_block(reinterpret_cast<const int8_t*>(X) + (size_t)c * 32, lo, hi, xs8);
 #pragma unroll
         for (int i = 0; i < 4; ++i) { xr[i] = lo[i]; xr[4 + i] = hi[i]; }
-        sx8 = __ldg(a.SX[it_comp] + c);
+        sx8 = a.SX[it_comp][c];
       }
       return;
     }
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kGdMaxWarps * 32) gemv_direct_async_kernel(con
       const uint4* xp = reinterpret_cast<const uint4*>(X + (size_t)c * 32);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const uint4 u = ld_nc_v4(xp + v);
+        const uint4 u = ld_v4(xp + v);
         xr[4 * v + 0] = u.x; xr[4 * v + 1] = u.y; xr[4 * v + 2] = u.z; xr[4 * v + 3] = u.w;
       }
 #pragma unroll

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kM1MaxConsumerThreads + 32, 2) gemv_m1_kernel(
           const uint4* xp = reinterpret_cast<const uint4*>(a.X + (size_t)(c0 + c) * 32);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const uint4 u = ld_nc_v4(xp + v);
+            const uint4 u = ld_v4(xp + v);
             xr[j][4 * v + 0] = u.x; xr[j][4 * v + 1] = u.y; xr[j][4 * v + 2] = u.z; xr[j][4 * v + 3] = u.w;
           }
 #pragma unroll

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__((kTmMaxSlices + 1) * 32, 1)
     x_loaded = X;
     const int cm = cbase + (g >> 1) + 4 * (g & 1);
     uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-    if (cm < chunks) xv = ld_nc_v4(X + (size_t)cm * 32 + 8 * t);
+    if (cm < chunks) xv = ld_v4(X + (size_t)cm * 32 + 8 * t);
     const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)

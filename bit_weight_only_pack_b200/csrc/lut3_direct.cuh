@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kLdMaxWarps * 32, 1) lut3_direct_kernel(const 
     const uint4* xp = reinterpret_cast<const uint4*>(a.X + (size_t)kt * 64);
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const uint4 u = ld_nc_v4(xp + v);
+      const uint4 u = ld_v4(xp + v);
       xr[4 * v + 0] = u.x; xr[4 * v + 1] = u.y; xr[4 * v + 2] = u.z; xr[4 * v + 3] = u.w;
     }
   } else {

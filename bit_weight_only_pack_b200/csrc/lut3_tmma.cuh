@@ -135,7 +135,7 @@ __global__ void __launch_bounds__((kL3tMaxWarps + 1) * 32, 1)
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (on) v = ld_nc_v4(xp + t);
+      if (on) v = ld_v4(xp + t);
       xb[i][t][0] = ((unsigned long long)v.y << 32) | v.x;
       xb[i][t][1] = ((unsigned long long)v.w << 32) | v.z;
     }

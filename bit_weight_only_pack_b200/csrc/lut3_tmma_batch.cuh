@@ -96,7 +96,7 @@ __global__ void __launch_bounds__((kL3tMaxWarps + 1) * 32, 1)
   float* red = reinterpret_cast<float*>(ring + a.red_off);       // [2][nw][16][8]
   griddep_wait();  // X may be written by the previous kernel in the stream
   for (int i = tid; i < M * K / 8; i += nthreads)
-    reinterpret_cast<uint4*>(xs)[i] = ld_nc_v4(reinterpret_cast<const uint4*>(a.X) + i);
+    reinterpret_cast<uint4*>(xs)[i] = ld_v4(reinterpret_cast<const uint4*>(a.X) + i);
   consumer_sync(nthreads);
 
   const int g = lane >> 2, t = lane & 3;

@@ -59,10 +59,11 @@ __device__ __forceinline__ void w8_griddep_launch_dependents() { asm volatile("g
 // everywhere, one division per block on the common path.
 // With programmatic dependent launch the GEMV that reads the codes may start
 // (and stream its weights) while this kernel runs; X is read only after the
-// previous kernel in the stream has finished.
+// previous kernel in the stream has finished (the pointers carry no __restrict__,
+// with which the compiler may read X above that wait).
 template <bool BF16>
-__global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __restrict__ X, int M, int K,
-                                                            int8_t* __restrict__ xq, float* __restrict__ sx) {
+__global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* X, int M, int K, int8_t* xq,
+                                                            float* sx) {
   w8_griddep_launch_dependents();
   w8_griddep_wait();
   const long long blk = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -89,8 +90,7 @@ __global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __re
 // orders (word i of a code chunk holds k = 8i .. 8i+7 as bytes (k0, k4, k1, k5)
 // of its low nibbles and (k2, k6, k3, k7) of its high nibbles) and their sum.
 __device__ __forceinline__ void load_xq_block(const int8_t* p, uint32_t (&xlo)[4], uint32_t (&xhi)[4], int& xsum) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  const uint4 a = ld_v4(p), b = ld_v4(p + 16);
   const uint32_t nat[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   xsum = 0;
 #pragma unroll
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kW8MaxWarps * 32) w4a8_gemv_kernel(const W4a8A
     for (int i = 0; i < 4; ++i) { xlo[m][i] = 0u; xhi[m][i] = 0u; }
     if (cok && m < a.m_valid) {
       load_xq_block(a.XQ + (size_t)m * a.K + (size_t)c * 32, xlo[m], xhi[m], xsum[m]);
-      sx[m] = __ldg(a.SX + (size_t)m * chunks + c);
+      sx[m] = a.SX[(size_t)m * chunks + c];
     }
   }
 

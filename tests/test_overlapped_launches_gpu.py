@@ -3,6 +3,8 @@ after another. Equality, bit for bit: the kernels and their orders are the same.
 
 import pytest
 
+import workloads
+
 pytestmark = pytest.mark.gpu
 
 
@@ -123,4 +125,63 @@ def test_routed_chain(torch, lbq, T, cluster):
             assert all(torch.equal(s, t) for s, t in zip(a, [*got, *b]))
     finally:
         lbq.lbq_debug_sort_cluster(False)
+    lbq.device_status()
+
+
+# (name, batch, the test hook's kernel choice)
+GEMVS = [*(("int4", 1, path) for path in (0, 1, 4, 5)), ("int4", 4, 2), ("int4", 4, 3), ("int4", 1, "registers"),
+         ("lut3", 1, 0), ("lut3", 1, 4), ("lut3", 4, 0), ("lut3", 16, 0), ("lut3", 4, 2), ("affine", 1, 0),
+         ("affine", 4, 0), ("w4a8", 1, 0), ("w4a8", 1, "tiled"), ("w4a8", 4, 0)]
+
+
+@pytest.mark.parametrize("name,M,path", GEMVS)
+def test_gemvs_with_two_buffers_in_turn(torch, lbq, name, M, path):
+    """The low-bit GEMVs, as the W8A8 layers above (W4A8 with its quantiser between)."""
+    K, N, n = 1024, 1032, 24
+    g = torch.Generator(device="cuda").manual_seed(M)
+    dt = torch.bfloat16 if name == "lut3" else torch.float16
+    if name == "lut3":
+        pack = lambda seed, k, m: lbq.pack_lut3(*(torch.from_numpy(v).cuda() for v in workloads.lut3_host(seed, k, m)))  # noqa: E731
+        call = lambda x, img, m, ws, y: lbq.lut3_gemm(x, img, m, ws=ws, Y=y)  # noqa: E731
+        space = lambda k, m: lbq.workspace(2, M, k, m, 0, "lut3")  # noqa: E731
+    elif name == "affine":
+        pack = lambda seed, k, m: lbq.pack_affine(torch.from_numpy(workloads.weights_host(seed, k, m)).cuda(), 64, 3)  # noqa: E731
+        call = lambda x, img, m, ws, y: lbq.affine_gemv(x, img, m, 64, 3, Y=y)  # noqa: E731
+        space = lambda k, m: None  # noqa: E731
+    else:
+        pack = lambda seed, k, m: lbq.pack(torch.from_numpy(workloads.weights_host(seed, k, m)).cuda(), 32, "asym")  # noqa: E731
+        if name == "int4":
+            call = lambda x, img, m, ws, y: lbq.gemv(x, img, m, 32, "asym", ws=ws, Y=y)  # noqa: E731
+            space = lambda k, m: lbq.workspace(0, M, k, m, 32, "asym")  # noqa: E731
+        else:
+            call = lambda x, img, m, ws, y: lbq.w4a8_gemv(*lbq.quantize_int8(x), img, m, 32, "asym", Y=y)  # noqa: E731
+            space = lambda k, m: None  # noqa: E731
+    images = pack(1, K, K), pack(2, K, N)
+    xs = [torch.randn((M, K), generator=g, device="cuda").to(dt) for _ in range(n)]
+    if isinstance(path, int):
+        lbq.lbq_debug_gemv_path(path)
+    elif path == "registers":
+        lbq.lbq_debug_direct_variant(0)
+    else:
+        lbq.lbq_debug_w4a8_tiled(True)
+    try:
+        buf = [torch.zeros((M, K), dtype=dt, device="cuda") for _ in range(2)]
+        ws = space(K, K), space(K, N)
+
+        def run(outs):
+            for i in range(n):
+                call(xs[i], images[0], K, ws[0], buf[i % 2])
+                call(buf[i % 2], images[1], N, ws[1], outs[i])
+            torch.cuda.synchronize()
+            return outs
+
+        want = run([torch.empty((M, N), dtype=dt, device="cuda") for _ in range(n)])
+        got = [torch.empty_like(y) for y in want]
+        for _ in range(3):
+            overlapped(lbq, lambda: run(got))
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+    finally:
+        lbq.lbq_debug_gemv_path(0)
+        lbq.lbq_debug_direct_variant(-1)
+        lbq.lbq_debug_w4a8_tiled(False)
     lbq.device_status()

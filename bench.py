@@ -1055,20 +1055,20 @@ STEP_KERNEL = ("gemv_tmma_kernel (gate/up) and gemv_direct_async_kernel (q/k/v, 
 STEP_SOURCES = ("gemv_tmma.cuh", "gemv_direct.cuh", "gemv_m1.cuh", "w4a8.cuh", "tma.cuh", "common.cuh",
                 "lbq.cu#tmma-plan", "lbq.cu#direct-plan")
 STEP_CAPTURE_HASHES = {
-    "gemv_tmma.cuh": "8cbbf88b681552a5",
-    "gemv_direct.cuh": "370710b80822d44e",
-    "gemv_m1.cuh": "a992f85dd1acbd76",
-    "w4a8.cuh": "9b2ae43b5bafb58f",
+    "gemv_tmma.cuh": "c4f8ddbaf2de563e",
+    "gemv_direct.cuh": "879cb9ca8d7a709f",
+    "gemv_m1.cuh": "3fc35799e2df075a",
+    "w4a8.cuh": "7f8baf9054824f41",
     "tma.cuh": "5f428384c68b0ba7",
-    "common.cuh": "6e369f75860e0aec",
+    "common.cuh": "798a4b08ccd24f0a",
     "lbq.cu#tmma-plan": "9cb96b64b3d66c78",
     "lbq.cu#direct-plan": "b62033ebadd8a276",
 }
 STEP_TRAFFIC = {
-    "c2qkv": (14980608, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
+    "c2qkv": (14980864, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
     "c2o": (9997056, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
-    "c2gateup": (70270976, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
-    "c2down": (34921728, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
+    "c2gateup": (70684416, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
+    "c2down": (34921472, STEP_CAPTURE_HASHES, "profiles/gemv_decode_step_shapes_4096x_asym_g32_m1.md"),
 }
 # the planner sections of lbq.cu (kernel choice, launch shape, K split, stages)
 PLAN_MARKERS = {"tmma-plan": ("// M = 1: TMA-fed warp-MMA GEMV", "// Scratch of that kernel for one call"),

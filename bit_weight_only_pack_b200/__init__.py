@@ -26,6 +26,6 @@ from .binding import (  # noqa: F401
     quantize_int8_rows, quantize_int8_weight, w8a8_gemm, w8a8_linear, moe_w8a8_gemm, lbq_quantize_int8_rows,
     lbq_quantize_int8_weight, lbq_w8a8_gemm, lbq_w8a8_linear, lbq_w8a8_workspace_size, lbq_moe_w8a8_gemm,
     moe_sort, moe_permute, moe_permute_grad, moe_combine, moe_combine_grad, lbq_moe_sort, lbq_moe_permute,
-    lbq_moe_combine, lbq_moe_combine_grad,
+    lbq_moe_combine, lbq_moe_combine_grad, lbq_moe_combine_grad_full,
     MOE_BLOCK, moe_align, moe_lut3_mx_gemm, pack_lut3_experts, lbq_moe_align, lbq_moe_lut3_mx_gemm, lbq_moe_max_padded,
 )

@@ -101,6 +101,7 @@ _SIGS = {
     "lbq_moe_permute": ([_vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp], _c_int),
     "lbq_moe_combine": ([_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp], _c_int),
     "lbq_moe_combine_grad": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
+    "lbq_moe_combine_grad_full": ([_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp], _c_int),
     "lbq_debug_w8a8_gemv_max": ([_c_int], None),
     "lbq_debug_w8a8_hold": ([_c_int], None),
     "lbq_debug_w8a8_plan": ([_c_int, _c_int, _c_int, _c_int], None),
@@ -410,6 +411,11 @@ def lbq_moe_combine(Ys, dtype, rows, H, row_of_pair, weights, T, top_k, out, str
 
 def lbq_moe_combine_grad(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, stream):
     _check(_lib.lbq_moe_combine_grad(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, stream))
+
+
+def lbq_moe_combine_grad_full(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, stream):
+    _check(_lib.lbq_moe_combine_grad_full(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights,
+                                          stream))
 
 
 def lbq_set_option(option, value):
@@ -990,8 +996,8 @@ def moe_combine(Ys, row_of_pair, weights=None, out=None):
 
 
 def moe_combine_grad(dout, Ys, row_of_pair, weights, dYs=None):
-    """Gradients of moe_combine: (dYs [rows, H], dweights float32 [T, top_k]). Rows of dYs that no entry names are
-    not written; dYs may be Ys itself."""
+    """Gradients of moe_combine: (dYs [rows, H], dweights float32 [T, top_k]). Rows that no entry names have the
+    gradient zero in a new dYs; in one that is given (it may be Ys itself) they are not written."""
     dev = _device(Ys, "Ys")
     code = _half_code(Ys, "Ys")
     if not (Ys.get_device() == dev and Ys.is_contiguous() and Ys.dim() == 2):
@@ -1007,14 +1013,15 @@ def moe_combine_grad(dout, Ys, row_of_pair, weights, dYs=None):
     if not (weights.dtype is _F32 and weights.get_device() == dev and weights.is_contiguous()
             and weights.shape == pairs):
         _arg(weights, "weights", _F32, 2, pairs, dev)
+    grad = _lib.lbq_moe_combine_grad
     if dYs is None:
         dYs = Ys.new_empty((rows, H))
+        grad = _lib.lbq_moe_combine_grad_full
     elif not (dYs.dtype is Ys.dtype and dYs.get_device() == dev and dYs.is_contiguous() and dYs.shape == (rows, H)):
         _arg(dYs, "dYs", Ys.dtype, 2, (rows, H), dev)
     dweights = weights.new_empty(pairs)
-    status = _lib.lbq_moe_combine_grad(dout.data_ptr(), Ys.data_ptr(), code, rows, H, row_of_pair.data_ptr(),
-                                       weights.data_ptr(), T, top_k, dYs.data_ptr(), dweights.data_ptr(),
-                                       _raw_stream(dev))
+    status = grad(dout.data_ptr(), Ys.data_ptr(), code, rows, H, row_of_pair.data_ptr(), weights.data_ptr(), T, top_k,
+                  dYs.data_ptr(), dweights.data_ptr(), _raw_stream(dev))
     if status:
         _check(status)
     return dYs, dweights

@@ -1834,6 +1834,57 @@ static const void* combine_kernel(int n, int top_k) {
                   : (const void*)moe_combine_kernel<BF16, 1, 4, 8>;
 }
 
+// The combine's gradient; with `full` the rows of dYs that no entry names are
+// zeroed too. Which those are is known on the device only. Either the grid's first
+// blocks read all the entries, each for its own rows, beside the tokens' blocks, or
+// all of dYs is zeroed before the kernel. Reading takes a block of 32 threads 1 us
+// per 1024 entries, which is hidden where rows are wide or pairs few (T = 4096
+// top-8: H = 2048 50 us against 70, 49 without zeroing; H = 1024 26 / 35 / 26; 256
+// tokens top-4, H = 1024 2.7 / 4.1 / 2.5), but not otherwise (T = 4096: H = 512 22 us
+// against 20, H = 64 31 against 8).
+static lbq_status run_combine_grad(const void* dout, const void* Ys, int dtype, int rows, int H,
+                                   const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
+                                   float* dweights, bool full, cudaStream_t stream) {
+  lbq_status st = check_routed(T, top_k, rows);
+  if (st != LBQ_OK) return st;
+  if (H <= 0) return fail(LBQ_ERR_INVALID_ARG, "H=%d must be positive", H);
+  if (dtype != LBQ_DTYPE_F16 && dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if (!dout || !Ys || !row_of_pair || !weights || !dYs || !dweights)
+    return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be non-null");
+  if (!aligned16(dout) || !aligned16(Ys) || !aligned16(row_of_pair) || !aligned16(weights) || !aligned16(dYs) ||
+      !aligned16(dweights))
+    return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be 16-byte aligned");
+  if (full && dYs == Ys) return fail(LBQ_ERR_INVALID_ARG, "dYs must not be Ys where unnamed rows are zeroed");
+  const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
+  const bool b = dtype == LBQ_DTYPE_BF16;
+  const void* fn = n == 8   ? (b ? (const void*)moe_combine_grad_kernel<true, 8, 1> : (const void*)moe_combine_grad_kernel<false, 8, 1>)
+                   : n == 4 ? (b ? (const void*)moe_combine_grad_kernel<true, 4, 2> : (const void*)moe_combine_grad_kernel<false, 4, 2>)
+                   : n == 2 ? (b ? (const void*)moe_combine_grad_kernel<true, 2, 4> : (const void*)moe_combine_grad_kernel<false, 2, 4>)
+                            : (b ? (const void*)moe_combine_grad_kernel<true, 1, 4> : (const void*)moe_combine_grad_kernel<false, 1, 4>);
+  int per_row = H / n;
+  bool pdl = g_pdl != 0;
+  const int u = n == 8 ? 1 : n == 4 ? 2 : 4;  // pieces per thread and step
+  const int block = std::min(256, std::max(32, (int)align_up((size_t)((per_row + u - 1) / u), 32)));
+  int zero_blocks = 0, zero_rows = 0;
+  if (full) {
+    const int most = (int)(((long long)rows + 31) / 32);  // blocks of 32 rows at least
+    zero_blocks = std::min(num_sms(), most);
+    zero_rows = (int)align_up(((size_t)rows + zero_blocks - 1) / zero_blocks, 32);
+    zero_blocks = (int)(((long long)rows + zero_rows - 1) / zero_rows);
+    if (zero_rows > kZeroRows || (block < 128 && (long long)T * top_k > 128LL * block)) {
+      const cudaError_t e = cudaMemsetAsync(dYs, 0, (size_t)rows * H * 2, stream);
+      if (e != cudaSuccess) return cuda_check(e, "zeroing the gradient's rows");
+      zero_blocks = 0;
+      pdl = false;
+    }
+  }
+  void* args[] = {(void*)&dout, (void*)&Ys, (void*)&rows, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
+                  (void*)&weights, (void*)&dYs, (void*)&dweights, (void*)&zero_blocks, (void*)&zero_rows};
+  return launch_kernel_ex(fn, dim3((unsigned)T + (unsigned)zero_blocks), dim3(block), 0, stream, pdl, args,
+                          "MoE combine gradient launch");
+}
+
+
 }  // namespace lbq
 
 using namespace lbq;
@@ -2616,28 +2667,15 @@ lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int
 lbq_status lbq_moe_combine_grad(const void* dout, const void* Ys, int dtype, int rows, int H,
                                 const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
                                 float* dweights, void* stream) {
-  lbq_status st = check_routed(T, top_k, rows);
-  if (st != LBQ_OK) return st;
-  if (H <= 0) return fail(LBQ_ERR_INVALID_ARG, "H=%d must be positive", H);
-  if (dtype != LBQ_DTYPE_F16 && dtype != LBQ_DTYPE_BF16) return fail(LBQ_ERR_UNSUPPORTED, "dtype %d", dtype);
-  if (!dout || !Ys || !row_of_pair || !weights || !dYs || !dweights)
-    return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be non-null");
-  if (!aligned16(dout) || !aligned16(Ys) || !aligned16(row_of_pair) || !aligned16(weights) || !aligned16(dYs) ||
-      !aligned16(dweights))
-    return fail(LBQ_ERR_INVALID_ARG, "dout, Ys, row_of_pair, weights, dYs and dweights must be 16-byte aligned");
-  const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
-  const bool b = dtype == LBQ_DTYPE_BF16;
-  const void* fn = n == 8   ? (b ? (const void*)moe_combine_grad_kernel<true, 8, 1> : (const void*)moe_combine_grad_kernel<false, 8, 1>)
-                   : n == 4 ? (b ? (const void*)moe_combine_grad_kernel<true, 4, 2> : (const void*)moe_combine_grad_kernel<false, 4, 2>)
-                   : n == 2 ? (b ? (const void*)moe_combine_grad_kernel<true, 2, 4> : (const void*)moe_combine_grad_kernel<false, 2, 4>)
-                            : (b ? (const void*)moe_combine_grad_kernel<true, 1, 4> : (const void*)moe_combine_grad_kernel<false, 1, 4>);
-  int per_row = H / n;
-  const int u = n == 8 ? 1 : n == 4 ? 2 : 4;  // pieces per thread and step
-  const int block = std::min(256, std::max(32, (int)align_up((size_t)((per_row + u - 1) / u), 32)));
-  void* args[] = {(void*)&dout, (void*)&Ys, (void*)&rows, (void*)&per_row, (void*)&top_k, (void*)&row_of_pair,
-                  (void*)&weights, (void*)&dYs, (void*)&dweights};
-  return launch_kernel_ex(fn, dim3((unsigned)T), dim3(block), 0, static_cast<cudaStream_t>(stream), g_pdl != 0, args,
-                          "MoE combine gradient launch");
+  return run_combine_grad(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, false,
+                          static_cast<cudaStream_t>(stream));
+}
+
+lbq_status lbq_moe_combine_grad_full(const void* dout, const void* Ys, int dtype, int rows, int H,
+                                     const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
+                                     float* dweights, void* stream) {
+  return run_combine_grad(dout, Ys, dtype, rows, H, row_of_pair, weights, T, top_k, dYs, dweights, true,
+                          static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -325,22 +325,69 @@ __global__ void __launch_bounds__(256, N == 8 ? 4 : 2) moe_combine_kernel(const 
   }
 }
 
+constexpr int kZeroRows = 8192;  // the most rows per zeroing block (a byte each in shared memory)
+
+// Zero the rows of dY among r0 .. r1 - 1 (at most kZeroRows) that no entry of
+// row_of_pair names: a mark per row, set from all the entries (a store each, of the
+// others to a place behind: a branch per entry takes twice as long), then a warp
+// per row.
+template <typename V>
+__device__ __forceinline__ void moe_zero_unnamed(V* dY, int per_row, const int32_t* row_of_pair, long long pairs, int r0,
+                                                 int r1) {
+  __shared__ uint32_t marks[kZeroRows / 4 + 1];
+  uint8_t* named = reinterpret_cast<uint8_t*>(marks);
+  const int tid = threadIdx.x, nt = blockDim.x;
+  for (int i = tid; i <= (r1 - r0) / 4; i += nt) marks[i] = 0u;
+  __syncthreads();
+  auto mark = [&](int r) {
+    named[min((uint32_t)r - (uint32_t)r0, (uint32_t)(r1 - r0))] = 1;
+  };
+  const int4* v = reinterpret_cast<const int4*>(row_of_pair);
+  const long long quads = pairs >> 2;
+  for (long long q = tid; q < quads; q += 8LL * nt) {
+    int4 r[8];  // requested together, then marked
+#pragma unroll
+    for (int u = 0; u < 8; ++u) r[u] = q + u * nt < quads ? v[q + u * nt] : make_int4(-1, -1, -1, -1);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      mark(r[u].x);
+      mark(r[u].y);
+      mark(r[u].z);
+      mark(r[u].w);
+    }
+  }
+  if (tid < (int)(pairs & 3)) mark(row_of_pair[4 * quads + tid]);
+  __syncthreads();
+  for (int r = r0 + (tid >> 5); r < r1; r += nt >> 5) {
+    if (named[r - r0]) continue;
+    V* y = dY + (size_t)r * per_row;
+    for (int i = tid & 31; i < per_row; i += 32) y[i] = V{};
+  }
+}
+
 // Block = one token. Its dout row is read once for every four choices; each
 // thread keeps its part of the four dot products, which meet in shared memory
 // in a fixed order. HBM-bound: 4096 tokens, top-8, H = 2048 49 us (5.8 TB/s), H =
 // 1002 29 (4.8), H = 1003 46 (3.0). dY may be Y (a thread reads a place before it writes it), so
-// neither is declared restrict.
+// neither is declared restrict. The grid's first zero_blocks blocks, if any, zero the rows of dY
+// that no entry names, zero_rows each; no other block touches those.
 template <bool BF16, int N, int U>
 __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* dout, const void* Y, int rows,
                                                                int per_row, int top_k,
                                                                const int32_t* row_of_pair,
                                                                const float* weights, void* dY,
-                                                               float* dweights) {
+                                                               float* dweights, int zero_blocks, int zero_rows) {
   using V = typename RowVec<2 * N>::T;
   __shared__ float red[4][8];
   w8_griddep_launch_dependents();
   w8_griddep_wait();
-  const long long t = blockIdx.x;
+  if ((int)blockIdx.x < zero_blocks) {
+    const int r0 = (int)blockIdx.x * zero_rows;
+    moe_zero_unnamed(static_cast<V*>(dY), per_row, row_of_pair, (long long)(gridDim.x - zero_blocks) * top_k, r0,
+                     min(rows, r0 + zero_rows));
+    return;
+  }
+  const long long t = blockIdx.x - zero_blocks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;
   const V* d = static_cast<const V*>(dout) + t * per_row;
   for (int j0 = 0; j0 < top_k; j0 += 4) {

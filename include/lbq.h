@@ -632,12 +632,16 @@ lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int
  *   dout (device) [T, H], Ys and dYs (device) [rows, H], `dtype`
  *   weights, dweights (device) float32 [T, top_k]
  * The entries of row_of_pair are different; skipped entries have dweights 0, and
- * rows of dYs that no entry names are not written. dYs may be Ys. Errors as
- * lbq_moe_combine. Asynchronous on `stream`.
+ * rows of dYs that no entry names are not written; dYs may be Ys.
+ * lbq_moe_combine_grad_full is the same, but zeroes those rows (their gradient);
+ * there dYs must not be Ys. Errors as lbq_moe_combine. Asynchronous on `stream`.
  */
 lbq_status lbq_moe_combine_grad(const void* dout, const void* Ys, int dtype, int rows, int H,
                                 const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
                                 float* dweights, void* stream);
+lbq_status lbq_moe_combine_grad_full(const void* dout, const void* Ys, int dtype, int rows, int H,
+                                     const int32_t* row_of_pair, const float* weights, int T, int top_k, void* dYs,
+                                     float* dweights, void* stream);
 
 /* Number of kernel launches the library has enqueued so far in this process. */
 uint64_t lbq_launch_count(void);

@@ -1641,9 +1641,11 @@ static int g_w8_gemv_max = kW8GvMaxM;  // test hook: largest M on the CUDA-core 
 template <bool QUANT, bool BF16>
 static const void* w8_gemv_kernel(int M) {
   if (M == 1) return (const void*)w8a8_gemv_kernel<1, QUANT, BF16>;
-  if (M == 2) return (const void*)w8a8_gemv_kernel<2, QUANT, BF16>;
-  if (M <= 4) return (const void*)w8a8_gemv_kernel<4, QUANT, BF16>;
-  return (const void*)w8a8_gemv_kernel<8, QUANT, BF16>;
+  if (QUANT || M == 2) return (const void*)w8a8_gemv_kernel<2, QUANT, BF16>;  // quantising: see w8_gemv_fused
+  if constexpr (!QUANT) {
+    if (M <= 4) return (const void*)w8a8_gemv_kernel<4, QUANT, BF16>;
+    return (const void*)w8a8_gemv_kernel<8, QUANT, BF16>;
+  }
 }
 
 // Whether M tokens of K codes go to the CUDA-core product: the codes of the
@@ -1657,7 +1659,7 @@ static bool w8_gemv_ok(int M, int K, int N) {
 // (One token: 4.8 us against 5.7 at K = N = 4096, 11.4 against 12.3 at N = 14336;
 // two: 5.8 against 6.1. Four: 8.4 against 7.5, the blocks then read too much of X.)
 static bool w8_gemv_fused(int M, int K) {
-  return M <= std::min(2, g_w8_gemv_max) && (long long)M * K <= kW8GvFusedVpt * 8 * kW8GvWarps * 32;
+  return M <= std::min(kW8GvFusedM, g_w8_gemv_max) && (long long)M * K <= kW8GvFusedVpt * 8 * kW8GvWarps * 32;
 }
 
 // x_dtype < 0: X holds codes with the scales sx.

@@ -206,6 +206,7 @@ constexpr int kW8GvWarps = 8;
 constexpr int kW8GvRows = 2;    // channels per warp at a time
 constexpr int kW8GvUnroll = 4;  // 16-byte chunks per lane and channel at a time
 constexpr int kW8GvMaxM = 8;
+constexpr int kW8GvFusedM = 2;    // the most tokens of the quantising form
 constexpr int kW8GvFusedVpt = 8;  // X chunks of 8 per thread that the quantising form keeps in registers
 
 struct W8GemvArgs {
@@ -233,6 +234,7 @@ struct W8GemvArgs {
 // at N = 14336 (dp4a-bound), hence the limits in w8_gemv_ok.
 template <int MB, bool QUANT, bool BF16>
 __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8GemvArgs a) {
+  static_assert(!QUANT || MB <= kW8GvFusedM, "no call quantises more tokens in the block");
   extern __shared__ __align__(16) uint8_t xs[];  // [MB][K] codes
   __shared__ uint32_t max_sh[MB][kW8GvWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

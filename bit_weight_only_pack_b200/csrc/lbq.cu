@@ -1957,8 +1957,6 @@ void lbq_debug_lut3_stages(int stages) { g_l3t_stages = (stages >= 1 && stages <
 // kernel instead of the TMA-fed batch kernel (0 = the library's choice).
 void lbq_debug_lut3_batch_off(int on) { g_l3b_off = on ? 1 : 0; }
 
-// Test hook (not in the public header): largest M of the W8A8 product on the
-// CUDA cores (0: none, every M on the tensor cores; -1: the library's choice).
 // Test hook (not in the public header): 1 = every sort on the clustered kernel (0 = the library's choice).
 void lbq_debug_sort_cluster(int on) { g_sort_work = on ? 0 : kSortBlockWork; }
 // Test hook (not in the public header): the tensor-core plan of the dense W8A8
@@ -1986,6 +1984,8 @@ void lbq_debug_w8a8_planned(int M, int K, int N, int* out) {
   const int v[7] = {p.cg, p.ht, p.n_tiles, p.bn, p.m_tiles, p.splits, p.sub};
   std::copy(v, v + 7, out);
 }
+// Test hook (not in the public header): largest M of the W8A8 product on the
+// CUDA cores (0: none, every M on the tensor cores; -1: the library's choice).
 void lbq_debug_w8a8_gemv_max(int m) { g_w8_gemv_max = m < 0 ? kW8GvMaxM : std::min(m, kW8GvMaxM); }
 
 // Test hook (not in the public header): prefill stream-K on (1, the library's

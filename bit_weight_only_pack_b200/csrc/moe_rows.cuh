@@ -8,7 +8,8 @@
 //   gradients:   dY[row(t, j)] = w[t][j] dout[t]
 //                dw[t][j]      = sum_h dout[t][h] Y[row(t, j)][h]     (FP32)
 //                dX[t]         = sum_j dXs[row(t, j)]   (combine with weights 1)
-// Every result is a function of its inputs alone: no atomics, fixed orders.
+// Every result is a function of its inputs alone: fixed orders, and no atomics but
+// the counts of moe_sort_kernel, whose sums do not depend on theirs.
 #pragma once
 
 #include "common.cuh"

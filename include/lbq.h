@@ -251,13 +251,15 @@ lbq_status lbq_device_status(void* stream);
 
 /*
  * Process-wide launch options.
- *   LBQ_OPT_PDL (value 0/1, default 0): launch the GEMV kernels with
- *   programmatic dependent launch. A kernel may then start, and stream its
- *   weight image, while the previous kernel in the stream is still running;
- *   it reads X and writes Y only after that kernel has completed. Enable it
- *   only when no preceding kernel in the stream writes the image (images are
- *   normally written once by lbq_pack and then only read), e.g. for the
- *   back-to-back projections of a decode step.
+ *   LBQ_OPT_PDL (value 0/1, default 0): launch the GEMV kernels, the INT8
+ *   quantisers of activations, the W8A8 products (dense and routed) and the
+ *   routed rows' kernels (lbq_moe_sort, _permute, _combine, _combine_grad)
+ *   with programmatic dependent launch. A kernel may then start, and stream
+ *   its weights, while the previous kernel in the stream is still running;
+ *   it reads everything else and writes only after that kernel has completed.
+ *   Enable it only when no preceding kernel in the stream writes the weights
+ *   (images are normally written once by lbq_pack and then only read), e.g.
+ *   for the back-to-back projections of a decode step.
  */
 typedef enum { LBQ_OPT_PDL = 1 } lbq_option;
 lbq_status lbq_set_option(int option, int value);

@@ -22,7 +22,7 @@ from .binding import (  # noqa: F401
     affine_gemv, pack_affine, unpack_affine_canonical, lbq_affine_gemv, lbq_affine_packed_size, lbq_pack_affine,
     lbq_unpack_affine_canonical, quantize_int8, w4a8_gemv, lbq_quantize_int8, lbq_w4a8_gemv,
     w4a8_gemv_grouped, lbq_w4a8_gemv_grouped, lbq_debug_w4a8_tiled, lbq_debug_lut3_stages, lbq_debug_lut3_batch_off, lbq_debug_gemm_stream_k, lbq_debug_gemm_hold, lbq_debug_gemm_schedule, lbq_debug_tile_coords, lbq_debug_w8a8_gemv_max, lbq_debug_w8a8_plan, lbq_debug_w8a8_planned, lbq_debug_w8a8_hold,
-    lbq_debug_sort_cluster, make_w4a8_items,
+    lbq_debug_sort_cluster, lbq_debug_device, make_w4a8_items,
     quantize_int8_rows, quantize_int8_weight, w8a8_gemm, w8a8_linear, moe_w8a8_gemm, lbq_quantize_int8_rows,
     lbq_quantize_int8_weight, lbq_w8a8_gemm, lbq_w8a8_linear, lbq_w8a8_workspace_size, lbq_moe_w8a8_gemm,
     moe_sort, moe_permute, moe_permute_grad, moe_combine, moe_combine_grad, lbq_moe_sort, lbq_moe_permute,

@@ -107,6 +107,7 @@ _SIGS = {
     "lbq_debug_w8a8_plan": ([_c_int, _c_int, _c_int, _c_int], None),
     "lbq_debug_w8a8_planned": ([_c_int, _c_int, _c_int, ctypes.POINTER(_c_int)], None),
     "lbq_debug_sort_cluster": ([_c_int], None),
+    "lbq_debug_device": ([_c_int, _c_int], None),
     "lbq_debug_force_splits": ([_c_int], None),
     "lbq_debug_force_skinny": ([_c_int], None),
     "lbq_debug_force_tc": ([_c_int], None),
@@ -325,6 +326,11 @@ def lbq_debug_w8a8_planned(M, K, N):
 def lbq_debug_sort_cluster(on):
     """Test hook: every sort on the clustered kernel."""
     _lib.lbq_debug_sort_cluster(1 if on else 0)
+
+
+def lbq_debug_device(dev, sms):
+    """Test hook: host code takes `dev` for the current device, with `sms` SMs (-1: as it is); launch nothing meanwhile."""
+    _lib.lbq_debug_device(int(dev), int(sms))
 
 
 def lbq_debug_gemm_stream_k(on):

@@ -7,6 +7,7 @@
 // the CUDA-core GEMV, 2 <= M <= 16 to the tensor-core skinny kernel, larger M
 // to the tcgen05 prefill GEMM; split-K is chosen when the row tiles alone
 // cannot fill the SMs.
+#include <array>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -68,15 +69,25 @@ static lbq_status launch_check(const char* what) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+constexpr int kMaxDevices = 64;  // whose properties are kept (a device past them: looked up each time)
+static int g_debug_device = -1, g_debug_sms = 0;  // test hook: take this number for the current device's, and its SMs
+
+static int current_device() {
+  if (g_debug_device >= 0) return g_debug_device;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return dev;
+}
+
 static int num_sms() {
-  static int sms = 0;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (sms <= 0) sms = 148;
-  });
+  static std::atomic<int> kept[kMaxDevices];
+  const int dev = current_device();
+  int sms = dev < kMaxDevices ? kept[dev].load(std::memory_order_relaxed) : 0;
+  if (sms > 0) return sms;
+  if (g_debug_device >= 0) sms = g_debug_sms;
+  else cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (sms <= 0) sms = 148;
+  if (dev < kMaxDevices) kept[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
@@ -127,10 +138,9 @@ static lbq_status check_header(const ImageHeader& h, int K, int N, int group, in
 static int occupancy_for(const void* fn, int block, int smem) {
   static std::mutex mu;
   static std::map<std::pair<const void*, int>, bool> raised;  // the limit is the function's on one device
-  static std::map<std::pair<const void*, long long>, int> cache;
+  static std::map<std::tuple<const void*, int, long long>, int> cache;
   std::lock_guard<std::mutex> lk(mu);
-  int dev = 0;
-  cudaGetDevice(&dev);
+  const int dev = current_device();
   if (!raised[{fn, dev}]) {
     int optin = 0;
     cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
@@ -139,7 +149,7 @@ static int occupancy_for(const void* fn, int block, int smem) {
     cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - (int)fa.sharedSizeBytes);
     raised[{fn, dev}] = true;
   }
-  auto key = std::make_pair(fn, (long long)smem * 4096 + block);
+  const auto key = std::make_tuple(fn, dev, (long long)smem * 4096 + block);
   auto itc = cache.find(key);
   if (itc != cache.end()) return itc->second;
   int occ = 0;
@@ -1465,29 +1475,32 @@ struct W8Plan {
 // Blocks of `splits` that fit on the device at once as clusters, one per SM
 // (SMs of one cluster share a GPC, so 4 and 8 leave some idle).
 static int w8_max_clusters(int splits) {
-  static int cached[kW8MaxSplits + 1];
-  static std::once_flag once;
-  std::call_once(once, [] {
-    const void* fn = (const void*)w8a8_gemm_kernel<1>;
-    occupancy_for(fn, kW8Threads, kW8SmemBudget);
-    for (int s = 2; s <= kW8MaxSplits; s *= 2) {
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3((unsigned)(s * 64));
-      cfg.blockDim = dim3(kW8Threads);
-      cfg.dynamicSmemBytes = kW8SmemBudget;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = (unsigned)s;
-      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&cached[s], fn, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        cached[s] = 0;
-      }
+  static std::mutex mu;
+  static std::map<int, std::array<int, kW8MaxSplits + 1>> kept;  // by device
+  std::lock_guard<std::mutex> lk(mu);
+  const auto found = kept.find(current_device());
+  if (found != kept.end()) return found->second[splits];
+  auto& most = kept[current_device()];
+  most.fill(0);
+  const void* fn = (const void*)w8a8_gemm_kernel<1>;
+  occupancy_for(fn, kW8Threads, kW8SmemBudget);
+  for (int s = 2; s <= kW8MaxSplits; s *= 2) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(s * 64));
+    cfg.blockDim = dim3(kW8Threads);
+    cfg.dynamicSmemBytes = kW8SmemBudget;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)s;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&most[s], fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      most[s] = 0;
     }
-  });
-  return cached[splits];
+  }
+  return most[splits];
 }
 
 // Channels are shared out to tiles in steps of this many (what divides N, up to 4).
@@ -1600,13 +1613,14 @@ static W8Plan choose_w8a8(long long M, int K, int N) {
 // The choice takes a few microseconds, so each thread keeps its last ones.
 static W8Plan plan_w8a8(int M, int K, int N) {
   struct Entry {
-    int M, K, N;
+    int dev, M, K, N;
     W8Plan plan;
   };
   thread_local Entry kept[64] = {};
+  const int dev = current_device();
   if (g_w8_force.cg) return choose_w8a8(M, K, N);
   Entry& e = kept[((unsigned)M * 0x9E3779B1u ^ (unsigned)K * 0x85EBCA6Bu ^ (unsigned)N * 0xC2B2AE35u) >> 26];
-  if (e.M != M || e.K != K || e.N != N) e = Entry{M, K, N, choose_w8a8(M, K, N)};
+  if (e.dev != dev || e.M != M || e.K != K || e.N != N) e = Entry{dev, M, K, N, choose_w8a8(M, K, N)};
   return e.plan;
 }
 
@@ -1976,6 +1990,13 @@ void lbq_debug_w8a8_plan(int cg, int n_tiles, int bn, int splits) {
 // token rows, so its waits run out (after about a second each); it writes nothing
 // and raises the flag that lbq_device_status() reports.
 void lbq_debug_w8a8_hold(int on) { g_w8_hold = on ? 1 : 0; }
+
+// Test hook (not in the public header): host code takes `dev` for the current device,
+// with `sms` SMs (-1: as it is). Nothing may be launched meanwhile.
+void lbq_debug_device(int dev, int sms) {
+  g_debug_device = dev < 0 ? -1 : dev;
+  g_debug_sms = sms;
+}
 
 // Test hook (not in the public header): the plan that the library would choose, as
 // {cg, ht, n_tiles, bn, m_tiles, splits, blocks per stage}.

@@ -207,6 +207,7 @@ constexpr int kW8GvRows = 2;    // channels per warp at a time
 constexpr int kW8GvUnroll = 4;  // 16-byte chunks per lane and channel at a time
 constexpr int kW8GvMaxM = 8;
 constexpr int kW8GvFusedM = 2;    // the most tokens of the quantising form
+constexpr int kW8GvAhead = 2;     // steps that it prefetches into L2
 constexpr int kW8GvFusedVpt = 8;  // X chunks of 8 per thread that the quantising form keeps in registers
 
 struct W8GemvArgs {
@@ -228,7 +229,9 @@ struct W8GemvArgs {
 // The first weights are requested before anything else: the block then waits for
 // the kernel before (which may write X), and, with QUANT, quantises the tokens
 // itself (every block the same: reading a few KB from L2 costs less than a kernel
-// in front). One token: 4.7 us at K = N = 4096 (12.6 on the tensor cores behind a
+// in front). There the early request brings the weights of two steps into L2 only,
+// and the loads follow those of X: X behind 64 KB of an SM's weights comes 1 us later
+// (K = N = 4096 5.7 us instead of 4.6; one step ahead 4.9). One token: 4.7 us at K = N = 4096 (12.6 on the tensor cores behind a
 // quantiser), 11.3 at N = 14336 (5.2 TB/s), 36.0 at 8192 x 28672 (6.5 TB/s). Eight
 // tokens: 9.4 us at K = N = 4096 against 11.9 on the tensor cores, but 22 against 15
 // at N = 14336 (dp4a-bound), hence the limits in w8_gemv_ok.
@@ -258,7 +261,27 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
     }
   };
   const bool any = pair < a.pairs;
-  if (any) request();
+  if constexpr (!QUANT) {
+    if (any) request();
+  } else {
+    int p = pair, t = step;
+#pragma unroll 1
+    for (int i = 0; i < kW8GvAhead && p < a.pairs; ++i) {
+#pragma unroll
+      for (int r = 0; r < kW8GvRows; ++r) {
+        const int8_t* row = a.wq + (size_t)min(p * kW8GvRows + r, a.N - 1) * a.K;
+#pragma unroll
+        for (int u = 0; u < kW8GvUnroll; ++u) {
+          const int c = (t * kW8GvUnroll + u) * 32 + lane;
+          if (c < chunks) asm volatile("prefetch.global.L2 [%0];" :: "l"(row + (size_t)c * 16));
+        }
+      }
+      if (++t == steps) {
+        t = 0;
+        p += stride;
+      }
+    }
+  }
 
   float sx[MB];
   w8_griddep_wait();
@@ -275,6 +298,7 @@ __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8G
         v[m][i] = m < a.M && c < xchunks ? ld_v4(xr + c) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
+    if (any) request();
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       uint32_t m2 = 0u;

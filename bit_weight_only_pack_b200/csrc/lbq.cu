@@ -1843,11 +1843,11 @@ static lbq_status rows_grid(int T, int per_row, int u, int* shift, unsigned* gri
 }
 
 template <bool BF16>
-static const void* combine_kernel(int n, int top_k) {
-  if (n == 8) return top_k > 4 ? (const void*)moe_combine_kernel<BF16, 8, 8, 1> : (const void*)moe_combine_kernel<BF16, 8, 4, 1>;
-  return n == 4   ? (const void*)moe_combine_kernel<BF16, 4, 4, 2>
-         : n == 2 ? (const void*)moe_combine_kernel<BF16, 2, 4, 4>
-                  : (const void*)moe_combine_kernel<BF16, 1, 4, 8>;
+static const void* combine_kernel(int n) {
+  return n == 8   ? (const void*)moe_combine_kernel<BF16, 8, 1>
+         : n == 4 ? (const void*)moe_combine_kernel<BF16, 4, 2>
+         : n == 2 ? (const void*)moe_combine_kernel<BF16, 2, 4>
+                  : (const void*)moe_combine_kernel<BF16, 1, 8>;
 }
 
 // The combine's gradient; with `full` the rows of dYs that no entry names are
@@ -2677,7 +2677,7 @@ lbq_status lbq_moe_combine(const void* Ys, int dtype, int rows, int H, const int
     return fail(LBQ_ERR_INVALID_ARG, "Ys, row_of_pair, weights and out must be 16-byte aligned");
   const int n = H % 8 == 0 ? 8 : H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
   const bool b = dtype == LBQ_DTYPE_BF16;
-  const void* fn = b ? combine_kernel<true>(n, top_k) : combine_kernel<false>(n, top_k);
+  const void* fn = b ? combine_kernel<true>(n) : combine_kernel<false>(n);
   int per_row = H / n, shift = 0;
   unsigned grid = 0;
   if ((st = rows_grid(T, per_row, n == 8 ? 1 : n == 4 ? 2 : n == 2 ? 4 : 8, &shift, &grid)) != LBQ_OK) return st;

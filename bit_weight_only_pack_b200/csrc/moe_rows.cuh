@@ -271,16 +271,20 @@ __device__ __forceinline__ typename RowVec<2 * N>::T pack_row(const float (&f)[N
 }
 
 // Threads of a block per token as in moe_permute_kernel; a piece is N columns: the
-// token's top_k rows summed in FP32, j ascending, rounded once, J rows times U
-// pieces in flight per thread. weights null: 1. HBM-bound on the scattered rows: 4096
-// tokens, top-8, H = 2048 26.5-28.3 us (5.3-5.7 TB/s; 29.5 with 79 registers and so
-// three blocks per SM instead of four, 34 with four rows in flight instead of eight);
-// H = 1004 18-20 us (4 TB/s), H = 1003 26-34 (2.2-2.9).
-template <bool BF16, int N, int J, int U>
-__global__ void __launch_bounds__(256, N == 8 ? 4 : 2) moe_combine_kernel(const void* Y, int rows, int T, int per_row,
+// token's top_k rows summed in FP32, j ascending, rounded once, kCombineRows rows
+// times U pieces in flight per thread. weights null: 1. HBM-bound on the scattered
+// rows: 4096 tokens, top-8, H = 2048 27.6 us (5.5 TB/s; with eight rows in flight,
+// which do not fit the registers of four blocks per SM, 28.8, and 29.3 with three
+// blocks). Registers are bounded to as many blocks per SM as pays: H = 1004 17.1 us
+// (four blocks; 19.6 with three), H = 1002 19.0 (29.3), H = 1003 29.6 (three blocks;
+// 43 with four, 53 with two).
+constexpr int kCombineRows = 4;
+template <bool BF16, int N, int U>
+__global__ void __launch_bounds__(256, N == 1 ? 3 : 4) moe_combine_kernel(const void* Y, int rows, int T, int per_row,
                                                           int top_k, const int32_t* row_of_pair,
                                                           const float* weights, void* out,
                                                           int shift) {
+  constexpr int J = kCombineRows;
   using V = typename RowVec<2 * N>::T;
   w8_griddep_launch_dependents();
   w8_griddep_wait();

@@ -1656,22 +1656,25 @@ template <bool QUANT, bool BF16>
 static const void* w8_gemv_kernel(int M) {
   if (M == 1) return (const void*)w8a8_gemv_kernel<1, QUANT, BF16>;
   if (QUANT || M == 2) return (const void*)w8a8_gemv_kernel<2, QUANT, BF16>;  // quantising: see w8_gemv_fused
-  if constexpr (!QUANT) {
-    if (M <= 4) return (const void*)w8a8_gemv_kernel<4, QUANT, BF16>;
-    return (const void*)w8a8_gemv_kernel<8, QUANT, BF16>;
-  }
+  if constexpr (!QUANT) return (const void*)w8a8_gemv_kernel<4, QUANT, BF16>;
 }
 
 // Whether M tokens of K codes go to the CUDA-core product: the codes of the
-// padded batch have to fit beside a second block on the SM.
+// padded batch have to fit beside a second block on the SM, and three or four tokens
+// need rows that fill a warp's loads, or few of them. With the quantiser, against the
+// tensor cores: four tokens K = N = 4096 7.6 us / 9.6, 2048 x 28672 15.2 / 14.5, 1024 x
+// 4096 5.7 / 5.7, but 1024 x 14336 9.3 / 7.6 and 512 x 28672 14.0 / 7.9; two 4096 5.9 /
+// 9.6, 512 x 28672 9.5 / 7.9; five tokens 4096 9.8 / 9.6, 2048 x 8192 10.7 / 8.5, 1024 x
+// 14336 12.7 / 7.6, ahead (by 5%) only at some shapes of 2^22 weights.
 static bool w8_gemv_ok(int M, int K, int N) {
-  const int mb = M <= 2 ? M : M <= 4 ? 4 : 8;
+  const int mb = M <= 2 ? M : 4;
   if (M > g_w8_gemv_max || (long long)mb * K > 100 * 1024) return false;
-  return M <= 4 || (long long)K * N <= (1LL << 25);
+  return M <= 2 || K >= 1536 || N <= 4096;
 }
 // ... and whether it quantises them itself, keeping them in registers meanwhile.
-// (One token: 4.8 us against 5.7 at K = N = 4096, 11.4 against 12.3 at N = 14336;
-// two: 5.8 against 6.1. Four: 8.4 against 7.5, the blocks then read too much of X.)
+// (One token: 4.6-4.8 us against 5.6 at K = N = 4096, 10.5 against 11.9 at N = 14336;
+// two: 5.6-6.1 against 6.1, 12.2 against 12.3. Four: 8.4 against 7.5, the blocks then
+// read too much of X.)
 static bool w8_gemv_fused(int M, int K) {
   return M <= std::min(kW8GvFusedM, g_w8_gemv_max) && (long long)M * K <= kW8GvFusedVpt * 8 * kW8GvWarps * 32;
 }
@@ -1691,7 +1694,7 @@ static lbq_status run_w8a8_gemv(const void* X, int x_dtype, const float* sx, int
   const void* fn = x_dtype < 0                    ? w8_gemv_kernel<false, false>(M)
                    : x_dtype == LBQ_DTYPE_BF16 ? w8_gemv_kernel<true, true>(M)
                                                : w8_gemv_kernel<true, false>(M);
-  const int mb = M <= 2 ? M : M <= 4 ? 4 : 8;
+  const int mb = M <= 2 ? M : 4;
   const int smem = mb * K;
   const int occ = std::min(2, occupancy_for(fn, kW8GvWarps * 32, smem));
   const int grid = std::min((a.pairs + kW8GvWarps - 1) / kW8GvWarps, num_sms() * occ);

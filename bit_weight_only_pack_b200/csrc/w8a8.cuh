@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) quantize_int8_weight_kernel(const float* 
 constexpr int kW8GvWarps = 8;
 constexpr int kW8GvRows = 2;    // channels per warp at a time
 constexpr int kW8GvUnroll = 4;  // 16-byte chunks per lane and channel at a time
-constexpr int kW8GvMaxM = 8;
+constexpr int kW8GvMaxM = 4;
 constexpr int kW8GvFusedM = 2;    // the most tokens of the quantising form
 constexpr int kW8GvAhead = 2;     // steps that it prefetches into L2
 constexpr int kW8GvFusedVpt = 8;  // X chunks of 8 per thread that the quantising form keeps in registers
@@ -231,10 +231,10 @@ struct W8GemvArgs {
 // itself (every block the same: reading a few KB from L2 costs less than a kernel
 // in front). There the early request brings the weights of two steps into L2 only,
 // and the loads follow those of X: X behind 64 KB of an SM's weights comes 1 us later
-// (K = N = 4096 5.7 us instead of 4.6; one step ahead 4.9). One token: 4.7 us at K = N = 4096 (12.6 on the tensor cores behind a
-// quantiser), 11.3 at N = 14336 (5.2 TB/s), 36.0 at 8192 x 28672 (6.5 TB/s). Eight
-// tokens: 9.4 us at K = N = 4096 against 11.9 on the tensor cores, but 22 against 15
-// at N = 14336 (dp4a-bound), hence the limits in w8_gemv_ok.
+// (K = N = 4096 5.7 us instead of 4.6; one step ahead 4.9). With the quantiser, one
+// token: 4.6-4.8 us at K = N = 4096 (9.4 on the tensor cores), 10.5-11.0 at N = 14336
+// (5.3-5.6 TB/s), 34.6 at 8192 x 28672 (6.8 TB/s); four: 7.5 (9.6), 15 (15). More tokens
+// are dp4a-bound and slower than the tensor cores: see w8_gemv_ok.
 template <int MB, bool QUANT, bool BF16>
 __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8GemvArgs a) {
   static_assert(!QUANT || MB <= kW8GvFusedM, "no call quantises more tokens in the block");

@@ -121,3 +121,25 @@ def test_routed_layer_steps(torch, lbq, T):
     hq, sh = lbq.quantize_int8_rows(h)
     q, s = w8a8.quantize_rows(h.float().cpu().numpy())
     assert np.array_equal(hq.cpu().numpy(), q) and np.array_equal(sh.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("tensor", [False, True])
+@pytest.mark.parametrize("K,N", [(16, 5000), (512, 4100), (1024, 8200), (1520, 4097), (1536, 8200), (2048, 100), (25600, 40), (25616, 40)])
+def test_one_to_five_tokens(torch, lbq, K, N, tensor):
+    """Both products on both sides of the library's choice between them; a row is the same in either and at any batch."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    wq = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    x = torch.randn((5, K), generator=g, device="cuda").bfloat16()
+    sw = torch.exp2(torch.rand(N, generator=g, device="cuda") * 4 - 12)
+    xq, sx = lbq.quantize_int8_rows(x)
+    n = lambda t: t.cpu().numpy()  # noqa: E731
+    ref = w8a8.matmul(n(xq), n(sx), n(wq), n(sw))
+    lbq.lbq_debug_w8a8_gemv_max(0 if tensor else -1)
+    try:
+        for M in (1, 2, 3, 4, 5):
+            y = lbq.w8a8_gemm(xq[:M], sx[:M], wq, sw)
+            assert torch.equal(y, lbq.w8a8_linear(x[:M], wq, sw))
+            tol = np.abs(ref[:M]) * ((1 + 2.0 ** -8) * (1 + 2.0 ** -24) ** 3 - 1)
+            assert (np.abs(y.double().cpu().numpy() - ref[:M]) <= tol).all()
+    finally:
+        lbq.lbq_debug_w8a8_gemv_max(-1)

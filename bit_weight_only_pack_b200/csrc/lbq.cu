@@ -1530,10 +1530,12 @@ static int w8_sub(int ht, int bn, int cg, int K, int extra) {
 // decides between all of them: the weights' HBM time and waves x ring stages x the
 // longest of a stage's MMAs, its issue and its loads (the longer of the two, and a
 // fifth of the other), plus what a wave, a launch's blocks, the last tile's
-// epilogue, a pair and a split cost once. The constants are fitted to 2000 timed
-// plans of 56 shapes (M 9..6233, K 144..14336, N 136..28672): estimates are 10% off
-// on average, and the plan they choose is 1.5% slower than the best of the timed
-// ones (at worst 11%).
+// epilogue, a pair and a split cost once. The constants were
+// fitted to 2000 timed plans of 56 shapes (M 9..6233, K 144..14336, N 136..28672) before
+// the kernel's last steps, so the estimates themselves are off by now. What counts, the
+// choice, was timed again on this kernel, 1167 plans of 40 shapes (M 10..4218, K
+// 128..14336, N 129..26688): the chosen plan is 1.8% slower than the best of the timed
+// ones on average, at worst 11% (312 x 560 x 712, 5.9 us against 5.3).
 static W8Plan g_w8_force{};  // test hook: the dense plan's cg, n_tiles, bn and splits (cg 0: the library's choice)
 
 static W8Plan w8_plan_of(int cg, long long n_tiles, int bn, int splits, long long M, int K, int N) {
@@ -1626,7 +1628,12 @@ static W8Plan plan_w8a8(int M, int K, int N) {
 
 // Routed: the rows of each expert are known on the device only, so the tile is
 // chosen for the mean run of an expert; the MMAs and copies of a shorter run are
-// cut to its rows.
+// cut to its rows. Timed with every tile at mean runs of 1..400 rows on three layers
+// (256 experts 2048 x 1024, 32 of 4096 x 2048, 64 of 1024 x 1000): the rule is 1.1% slower
+// than the best tile on average, at worst 9%. Of 256 experts, us in tiles of 16 / 32 rows: mean 4
+// 82 / 81, 12 92 / 88; of 32 / 64: 12 88 / 88, 24 95 / 91; of 64 alone / 128 in pairs: 40
+// 95 / 94, 49 99 / 98, 64 106 / 99; pairs with 128 / 256: 96 106 / 107, 128 114 / 112, 256
+// 166 / 147 (shallow layers switch later: 64 experts 1024 x 1000, mean 192 26.8 / 29.2).
 static W8Plan plan_moe_w8a8(int M, int K, int N, int E) {
   W8Plan p{};
   const int mean = (M + E - 1) / E;

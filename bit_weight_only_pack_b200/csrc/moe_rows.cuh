@@ -223,7 +223,7 @@ template <> struct RowVec<1> { using T = uint8_t; };
 // Copies a token's row, read once, to its top_k places; U pieces per thread and
 // step, so that narrow pieces (rows that 16 bytes do not divide) still have
 // several loads in flight. HBM-bound: 4096 tokens, top-8, rows of 4 KB 25.6 us (5.9
-// TB/s); rows of 2006 bytes (2-byte pieces, top-2) 7.4 us (3.3 TB/s; 11.2 with four
+// TB/s); rows of 2006 bytes (2-byte pieces, top-2) 7.8 us (3.1 TB/s; 11.2 with four
 // pieces per thread instead of eight).
 template <int B, int U>
 __global__ void __launch_bounds__(256) moe_permute_kernel(const void* X, int T, int per_row, int top_k,
@@ -373,9 +373,10 @@ __device__ __forceinline__ void moe_zero_unnamed(V* dY, int per_row, const int32
 // Block = one token. Its dout row is read once for every four choices; each
 // thread keeps its part of the four dot products, which meet in shared memory
 // in a fixed order. HBM-bound: 4096 tokens, top-8, H = 2048 49 us (5.8 TB/s), H =
-// 1002 29 (4.8), H = 1003 46 (3.0). dY may be Y (a thread reads a place before it writes it), so
-// neither is declared restrict. The grid's first zero_blocks blocks, if any, zero the rows of dY
-// that no entry names, zero_rows each; no other block touches those.
+// 1002 30 (4.6), H = 1003 46 (3.0). dY may be Y (a thread reads a place before it
+// writes it), so neither is declared restrict. The grid's first zero_blocks blocks,
+// if any, zero the rows of dY that no entry names, zero_rows each; no other block
+// touches those.
 template <bool BF16, int N, int U>
 __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const void* dout, const void* Y, int rows,
                                                                int per_row, int top_k,

@@ -158,7 +158,9 @@ __global__ void __launch_bounds__(1024) quantize_int8_rows_kernel(const uint16_t
 
 // FP32 weight [K][N] -> codes [N][K] and a scale per channel, by the same rule.
 // Block = 32 channels x 8 k rows; pass 1 the channels' maxima, pass 2 the codes,
-// turned through a 32 x 32 tile so that both sides are read and written in rows.
+// turned through a 32 x 32 tile so that both sides are read and written in rows. Run
+// once per weight, so built for being simple: W is read twice, by N / 32 blocks (K = N
+// = 4096 264 us, 4096 x 14336 444, 8192 x 28672 979, 0.3-1.2 TB/s of W and codes).
 __global__ void __launch_bounds__(256) quantize_int8_weight_kernel(const float* W, int K, int N,
                                                                    int8_t* wq, float* sw) {
   __shared__ float red[8][32];
@@ -232,8 +234,8 @@ struct W8GemvArgs {
 // in front). There the early request brings the weights of two steps into L2 only,
 // and the loads follow those of X: X behind 64 KB of an SM's weights comes 1 us later
 // (K = N = 4096 5.7 us instead of 4.6; one step ahead 4.9). With the quantiser, one
-// token: 4.6-4.8 us at K = N = 4096 (9.4 on the tensor cores), 10.5-11.0 at N = 14336
-// (5.3-5.6 TB/s), 34.6 at 8192 x 28672 (6.8 TB/s); four: 7.5 (9.6), 15 (15). More tokens
+// token: 4.6-5.7 us at K = N = 4096 (9.4 on the tensor cores), 10.5-12.0 at N = 14336
+// (4.9-5.6 TB/s), 34.6 at 8192 x 28672 (6.8 TB/s); four: 7.5 (9.6), 15 (15). More tokens
 // are dp4a-bound and slower than the tensor cores: see w8_gemv_ok.
 template <int MB, bool QUANT, bool BF16>
 __global__ void __launch_bounds__(kW8GvWarps * 32, 2) w8a8_gemv_kernel(const W8GemvArgs a) {
@@ -849,10 +851,11 @@ __device__ __forceinline__ void w8_epilogue(uint32_t taddr, int half, int mh, fl
 // shared memory once per pair. The first block issues the MMAs; copies of both
 // are counted on its barrier, and its commits arrive in both blocks.
 //
-// Measured (K = 4096, N = 14336 unless stated): 16 tokens 13.9 us, 64 14.6, 512
-// 29.0 (2.07 P operations/s), 2048 82.7 (2.91), 8192 310 (3.1, 92% of twice the
-// measured BF16 rate; CG = 1 takes 348); 16 tokens at 8192 x 28672 40.7 us (5.8
-// TB/s); routed, 32768 rows over 256 experts of 2048 x 1024, 118 us (5.7 TB/s).
+// Measured (K = 4096, N = 14336 unless stated): 16 tokens 13.8 us, 64 14.3, 512
+// 29.4 (2.05 P operations/s), 2048 79-83 (2.9-3.05), 8192 295-310 (3.1-3.26, 92-96% of
+// twice the measured BF16 rate; CG = 1 takes 348); 16 tokens at 8192 x 28672 41.5 us
+// (5.7 TB/s); routed, 32768 rows over 256 experts of 2048 x 1024, 113-118 us (5.7-5.9
+// TB/s).
 template <int CG>
 __global__ void __launch_bounds__(kW8Threads, 1)
     w8a8_gemm_kernel(const __grid_constant__ W8Maps maps, const W8a8Args a) {

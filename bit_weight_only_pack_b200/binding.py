@@ -307,7 +307,7 @@ def lbq_debug_w8a8_gemv_max(m):
 
 
 def lbq_debug_w8a8_plan(cg, n_tiles=1, bn=16, splits=1):
-    """Test hook: force the dense W8A8 tensor-core plan (cg = 0: the library's choice)."""
+    """Test hook: force the W8A8 products' tensor-core plan (cg = 0: the library's choice)."""
     _lib.lbq_debug_w8a8_plan(cg, n_tiles, bn, splits)
 
 

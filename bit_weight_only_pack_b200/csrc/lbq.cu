@@ -1536,7 +1536,7 @@ static int w8_sub(int ht, int bn, int cg, int K, int extra) {
 // choice, was timed again on this kernel, 1167 plans of 40 shapes (M 10..4218, K
 // 128..14336, N 129..26688): the chosen plan is 1.8% slower than the best of the timed
 // ones on average, at worst 11% (312 x 560 x 712, 5.9 us against 5.3).
-static W8Plan g_w8_force{};  // test hook: the dense plan's cg, n_tiles, bn and splits (cg 0: the library's choice)
+static W8Plan g_w8_force{};  // test hook: the plans' cg, n_tiles, bn and splits (cg 0: the library's choice)
 
 static W8Plan w8_plan_of(int cg, long long n_tiles, int bn, int splits, long long M, int K, int N) {
   const int unit = w8_unit(N);
@@ -1983,9 +1983,10 @@ void lbq_debug_lut3_batch_off(int on) { g_l3b_off = on ? 1 : 0; }
 
 // Test hook (not in the public header): 1 = every sort on the clustered kernel (0 = the library's choice).
 void lbq_debug_sort_cluster(int on) { g_sort_work = on ? 0 : kSortBlockWork; }
-// Test hook (not in the public header): the tensor-core plan of the dense W8A8
-// product: blocks per MMA (1 or 2; 0: the library's choice), tiles along N, tokens
-// per tile, blocks sharing K. A plan that the shape cannot take fails the call.
+// Test hook (not in the public header): the tensor-core plan of the W8A8
+// products: blocks per MMA (1 or 2; 0: the library's choice), tiles along N, tokens
+// per tile, blocks sharing K (1 in the routed product, which takes the others too).
+// A plan that the shape cannot take fails the call.
 void lbq_debug_w8a8_plan(int cg, int n_tiles, int bn, int splits) {
   g_w8_force = W8Plan{};
   if ((cg == 1 || cg == 2) && n_tiles > 0 && bn > 0 &&

@@ -92,20 +92,29 @@ def test_many_rows(torch, lbq, T, H):
     assert torch.equal(dY, want) and torch.equal(dw, dw2)
 
 
-def test_in_a_graph(torch, lbq):
-    """Captured and replayed with other routings: rows named before are zero once nothing names them."""
+@pytest.mark.parametrize("overlap", [0, 1])
+@pytest.mark.parametrize("T,H", [(90, 256), (2000, 64)])
+def test_in_a_graph(torch, lbq, T, H, overlap):
+    """Captured and replayed with other routings: rows named before are zero once nothing names them. (Zeroed beside the
+    tokens and before them; with overlapping launches too.)"""
     g = torch.Generator(device="cuda").manual_seed(3)
-    T, top_k, E, H = 90, 4, 8, 256
+    top_k, E = 8, 8
     Y, dout = (torch.randn((n, H), generator=g, device="cuda").bfloat16() for n in (T * top_k, T))
     w = torch.rand((T, top_k), generator=g, device="cuda")
     row = lbq.moe_sort(torch.zeros((T, top_k), dtype=torch.int32, device="cuda"), E)[0]
     graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        dY, dw = lbq.moe_combine_grad(dout, Y, row, w)
+    lbq.lbq_set_option(lbq.LBQ_OPT_PDL, overlap)
+    try:
+        with torch.cuda.graph(graph):
+            lbq.moe_permute_grad(Y, row)
+            dY, dw = lbq.moe_combine_grad(dout, Y, row, w)
+            dX = lbq.moe_permute_grad(dY, row)
+    finally:
+        lbq.lbq_set_option(lbq.LBQ_OPT_PDL, 0)
     for keep in (E, 1, E // 2, 0):
         ids = torch.randint(0, E, (T, top_k), generator=g, device="cuda", dtype=torch.int32)
         row.copy_(lbq.moe_sort(torch.where(ids < keep, ids, -1), E)[0])
         graph.replay()
         torch.cuda.synchronize()
         want, dw2 = lbq.moe_combine_grad(dout, Y, row, w, dYs=torch.zeros_like(Y))
-        assert torch.equal(dY, want) and torch.equal(dw, dw2)
+        assert torch.equal(dY, want) and torch.equal(dw, dw2) and torch.equal(dX, lbq.moe_permute_grad(want, row))
